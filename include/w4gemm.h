@@ -241,6 +241,91 @@ typedef struct {
 int w4_linear_grouped(const uint16_t* x, const w4_parent* parents, int nparents, int T, int K,
                       int group, void* stream);
 
+/* ---- microscaled (MX) formats, after the OCP Microscaling Formats specification, v1.0.
+ * 32 consecutive columns share one scale 2^(byte - 127) (E8M0; byte 255 is NaN).  Elements:
+ *   W4_MXFP4  E2M1, codes 0 .. 7 = 0 0.5 1 1.5 2 3 4 6, bit 3 the sign; two to a byte, the even column
+ *             in the low nibble;
+ *   W4_MXFP8  E4M3 (largest 448), one to a byte.
+ * Quantising a block with largest magnitude m: byte = max(floor(log2 m) - emax + 127, 0), emax = 2
+ * (E2M1) or 8 (E4M3); code = the element nearest to v / 2^(byte - 127), ties to even, saturated.  A
+ * block of zeros has byte 0; a block that holds an infinity or NaN has byte 255 and codes 0, and
+ * everything computed from it is NaN.
+ *
+ * Weights are MXFP4.  Canonical (host) form: codes [N][K/2], scale bytes [N][K/32].  Packed (device)
+ * form, row tiles of 16 rows and k-blocks of 128 columns, KB = ceil(K / 128): codes
+ * [N/16][KB][64 lanes][16 bytes] and scale bytes [N/16][KB][64 lanes]; lane l holds row l % 16, columns
+ * 32 (l / 16) .. + 31 of the k-block, in canonical order.  Columns past K are zeros.  A SwiGLU pair
+ * interleaves the row tiles of gate and up as w4_repack_pair does.
+ *
+ * Activations are quantised to either format into a workspace: codes row-major [T][K * fmt / 8], then
+ * scale bytes [T][S], S = 16 * ceil(K / 512) (bytes past K / 32 are 0).  With MXFP4 and K a multiple of
+ * 512 a workspace is also the canonical form of a T x K weight matrix.
+ *
+ * K is a multiple of 32 and N of 16; T is any number of tokens (T == 0 is a successful no-op).
+ * 16-bit tensors are fp16 or bf16 (`dtype`).  W4_ERR_UNSUPPORTED for an unknown fmt or dtype;
+ * otherwise validation, errors and asynchrony as the calls above.
+ * These calls are additions of this library: no passage of the pages describes them. */
+#define W4_MXFP4 4
+#define W4_MXFP8 8
+#define W4_FP16 0
+#define W4_BF16 1
+
+size_t w4_mx_packed_bytes(int N, int K);            /* packed codes; 0 if the shape is invalid  */
+size_t w4_mx_packed_scale_bytes(int N, int K);      /* packed scales; 0 if the shape is invalid */
+size_t w4_mx_workspace_bytes(int T, int K, int fmt); /* 0 if the shape or format is invalid     */
+
+/* Host memory in, host memory out, bit-exact (as w4_repack / w4_repack_pair). */
+int w4_mx_repack(const uint8_t* codes, const uint8_t* scales, int N, int K, void* w_out,
+                 uint8_t* scales_out);
+int w4_mx_repack_pair(const uint8_t* gate_codes, const uint8_t* gate_scales, const uint8_t* up_codes,
+                      const uint8_t* up_scales, int N, int K, void* w_pair_out,
+                      uint8_t* scales_pair_out);
+
+/* x [T][K] (rows ldx elements apart, ldx >= K, a multiple of 8) -> workspace; and a workspace -> out
+ * [T][K], each value rounded once (NaN for a block of scale byte 255). */
+int w4_quantize_mx(const uint16_t* x, int64_t ldx, int T, int K, int fmt, int dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+int w4_dequantize_mx(const void* workspace, size_t workspace_bytes, int T, int K, int fmt, int dtype,
+                     uint16_t* out, void* stream);
+
+/* out[T][N] = round(X . W^T), round(silu(X . Wg^T) * (X . Wu^T)), round(X . W^T + R), X quantised to
+ * fmt and W MXFP4, sums in fp32, one rounding to dtype.  x may be NULL: the workspace then already
+ * holds this T x K activation, as w4_quantize_mx or w4_rmsnorm_mx wrote it.  Products of E4M3
+ * elements are aligned inside the matrix unit to the largest of a few neighbours and lose what lies
+ * about 2^-15 below it; products of E2M1 elements are summed exactly inside a step.
+ * out == residual (exactly) is allowed. */
+int w4_linear_mx(const uint16_t* x, const void* w, const uint8_t* scales, int T, int N, int K, int fmt,
+                 int dtype, uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+int w4_linear_swiglu_mx(const uint16_t* x, const void* w_pair, const uint8_t* scales_pair, int T, int N,
+                        int K, int fmt, int dtype, uint16_t* out, void* workspace,
+                        size_t workspace_bytes, void* stream);
+int w4_linear_add_mx(const uint16_t* x, const void* w, const uint8_t* scales, const uint16_t* residual,
+                     int T, int N, int K, int fmt, int dtype, uint16_t* out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* ---- root-mean-square norm, with the residual's addition in front of it:
+ *   h = x + residual,   y = h / sqrt(mean(h^2) + eps) * weight     (per token row, in fp32)
+ * residual_out = round(h); y, from the unrounded h, is rounded once: to dtype (w4_rmsnorm, any K), to
+ * the A8 route's int8 codes and scales (w4_rmsnorm_a8, K a multiple of 64; w4_linear_a8 and its
+ * siblings then take x == NULL) or to an MX workspace (w4_rmsnorm_mx, K a multiple of 32;
+ * w4_linear_mx and its siblings then take x == NULL).  A8 groups that hold an infinity or NaN get it
+ * as their scale.
+ * x: [T][K], rows ldx >= K elements apart; residual and residual_out: [T][K], both or neither;
+ * weight: [K].  residual_out and out may each be x (with ldx == K) or residual exactly; other overlaps
+ * are W4_ERR_ALIAS.  eps is finite and not negative. */
+int w4_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* residual, const uint16_t* weight,
+               float eps, int T, int K, int dtype, uint16_t* residual_out, uint16_t* out, void* stream);
+int w4_rmsnorm_a8(const uint16_t* x, int64_t ldx, const uint16_t* residual, const uint16_t* weight,
+                  float eps, int T, int K, int dtype, uint16_t* residual_out, void* workspace,
+                  size_t workspace_bytes, void* stream);
+int w4_rmsnorm_mx(const uint16_t* x, int64_t ldx, const uint16_t* residual, const uint16_t* weight,
+                  float eps, int T, int K, int fmt, int dtype, uint16_t* residual_out, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* An A8 workspace (w4_quantize_a8 or w4_rmsnorm_a8) back to 16 bits: out[T][K] = round(q * s). */
+int w4_dequantize_a8(const void* workspace, size_t workspace_bytes, int T, int K, int dtype,
+                     uint16_t* out, void* stream);
+
 /* ---- per-verify-width graphs: launch-overhead removal for decode steps.  A decode round calls
  * the same projections at a few token widths (concurrency x (draft + 1)); at one stream the
  * gaps and ramp-up/drain between short kernels are a large part of the step (ninfer-3080

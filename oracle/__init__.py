@@ -6,7 +6,8 @@ TEST INFRASTRUCTURE ONLY.  Only the tests, ``__graft_entry__.smoke()`` and the
 oracle reads the canonical weight format directly and never the repacked
 device layout.
 
-Every function here is pinned by ``tests/test_oracle_pins.py`` against things
+Every function here is pinned by ``tests/test_oracle_pins.py`` (the MX formats and the norm:
+``tests/test_mx_cpu.py``) against things
 fixed outside the oracle (exact rational brute force, literal byte fixtures,
 closed forms, integer matmul special cases, and the invariants the pages
 state).  See ``oracle.reference`` for the definitions and their sources.
@@ -24,4 +25,15 @@ from .reference import (  # noqa: F401
     quantize_a8,
     linear_a8,
     rel_l2,
+)
+from .mx import (  # noqa: F401
+    linear_mx,
+    mx_elements,
+    mx_value,
+    nearest_code,
+    pack_fp4,
+    quantize_mx,
+    rmsnorm,
+    swiglu_mx,
+    unpack_fp4,
 )

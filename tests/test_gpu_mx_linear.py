@@ -1,0 +1,302 @@
+"""GPU tier: the MX products against the fp64 oracle of the same quantised operands.
+
+Tolerances.  Quantisation is bit-exact, so what differs is the summation and the final rounding.
+Sums of E2M1 products inside a matrix-core step are exact up to fp32; a step's result is added to
+an fp32 accumulator, ceil(K / 128) times and a few more across waves: (ceil(K / 128) + 16) * 2^-24 of
+sum |p|.  E4M3 products lose what lies 2^-15 below the largest of a few neighbours (up to 8): 2^-12 of
+sum |p| more.  A SwiGLU output moves by at most |up| * 1.1 * (gate's error) + |silu(gate)| * (up's), and
+2^-20 relatively in exp, the division and the product.  Then half a step of the output type."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import w4_groupwise_gemm_amd as w4
+from test_gpu_mx_quant import DTYPES, exact64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+OPS = ["linear", "swiglu", "add"]
+TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+
+
+class Case:
+    def __init__(self, op, T, N, K, dtype, fmt, seed=0):
+        rng = np.random.default_rng(seed + 7 * T + 31 * N + K)
+        self.op, self.T, self.N, self.K, self.fmt, self.dtype = op, T, N, K, fmt, DTYPES[dtype]
+        self.weights = [(rng.integers(0, 16, (N, K)).astype(np.uint8), rng.integers(117, 122, (N, K // 32)).astype(np.uint8))
+                        for _ in range(2 if op == "swiglu" else 1)]
+        x = rng.standard_normal((T, K)) * np.exp2(rng.integers(-3, 3, (T, 1)))
+        x[:, rng.integers(0, K, max(1, K // 640))] *= 30
+        self.x = torch.from_numpy(x).to(self.dtype).to(DEV)
+        self.r = torch.from_numpy(rng.standard_normal((T, N))).to(self.dtype).to(DEV) if op == "add" else None
+        packed = [(oracle.pack_fp4(c), e) for c, e in self.weights]
+        self.pw = w4.pack_mx_pair(*packed, device=DEV) if op == "swiglu" else w4.pack_mx(*packed[0], device=DEV)
+
+    def run(self, x=None, **kw):
+        x = self.x if x is None else x
+        if self.op == "swiglu":
+            return w4.linear_swiglu_mx(x, self.pw, **kw)
+        if self.op == "add":
+            return w4.linear_add_mx(x, self.pw, self.r, **kw)
+        return w4.linear_mx(x, self.pw, **kw)
+
+    def reference(self, dtype=None):
+        """(the exact result, the bound of each element's error)"""
+        dtype = dtype or self.dtype
+        a = oracle.mx_value(*oracle.quantize_mx(exact64(self.x), self.fmt), self.fmt)
+        ws = [oracle.mx_value(c, e, 4) for c, e in self.weights]
+        p = [a @ w.T for w in ws]
+        rel = (-(-self.K // 128) + 16) * 2.0 ** -24 + (2.0 ** -12 if self.fmt == 8 else 0)
+        d = [np.abs(a) @ np.abs(w).T * rel for w in ws]
+        if self.op == "swiglu":
+            s = oracle.silu(p[0])
+            y = s * p[1]
+            tol = np.abs(p[1]) * 1.1 * d[0] + np.abs(s) * d[1] + 1.1 * d[0] * d[1] + np.abs(y) * 2.0 ** -20
+        else:
+            y = p[0] + (exact64(self.r) if self.op == "add" else 0)
+            tol = d[0] + np.abs(y) * 2.0 ** -24
+        return y, tol + (np.abs(y) + tol) * torch.finfo(dtype).eps / 2 + TINY[dtype]
+
+    def check(self, got, dtype=None):
+        y, tol = self.reference(dtype)
+        g = exact64(got)
+        lim = torch.finfo(dtype or self.dtype).max
+        sure = np.abs(y) + tol < lim  # a result past the type's largest may round to infinity
+        assert sure.mean() > 0.99
+        bad = sure & ~(np.abs(g - y) <= tol)
+        assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4], g[bad][:4], y[bad][:4], tol[bad][:4])
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("fmt", [4, 8])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 100, 130, 257])
+def test_every_width(op, T, fmt):
+    dtype = "fp16" if (T + fmt // 4) % 2 else "bf16"
+    c = Case(op, T, 80, 544, dtype, fmt)
+    c.check(c.run(fmt=fmt))
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("N,K", [(16, 32), (16, 64), (32, 96), (48, 128), (256, 512), (272, 640), (336, 1056),
+                                 (16, 5120), (1040, 256), (64, 5152), (4112, 160)])
+def test_shapes(op, N, K):
+    for T, dtype, fmt in ((1, "fp16", 8), (7, "bf16", 4), (40, "fp16", 4), (200, "bf16", 8)):
+        print(f"case {op} N={N} K={K} T={T} {dtype} fp{fmt}", flush=True)
+        c = Case(op, T, N, K, dtype, fmt)
+        c.check(c.run(fmt=fmt))
+
+
+@pytest.mark.parametrize("T,N,K,op,dtype,fmt", [
+    (4, 12288, 5120, "linear", "fp16", 8), (1, 5120, 17408, "add", "bf16", 4), (33, 2048, 5120, "swiglu", "bf16", 8),
+    (700, 1280, 2048, "add", "fp16", 4), (1500, 528, 1120, "linear", "bf16", 8), (600, 400, 2080, "swiglu", "fp16", 4)])
+def test_large(T, N, K, op, dtype, fmt):
+    c = Case(op, T, N, K, dtype, fmt)
+    c.check(c.run(fmt=fmt))
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("T", [1, 9, 30, 70, 300])
+def test_quantised_input_gives_the_same_bits(op, T):
+    for fmt in (4, 8):
+        c = Case(op, T, 96, 672, "fp16", fmt)
+        q = w4.quantize_mx(c.x, fmt=fmt)
+        assert torch.equal(c.run(q, dtype=torch.float16), c.run(fmt=fmt))
+        if op != "add":
+            c.check(c.run(q, dtype=torch.bfloat16), torch.bfloat16)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 200])
+def test_residual_in_place_workspace_and_guard_rows(T):
+    c = Case("add", T, 64, 288, "fp16", 8)
+    want = c.run()
+    buf = torch.full((T + 20, 64), 3.0, dtype=torch.float16, device=DEV)
+    buf[:T] = c.r
+    c.r = buf[:T]
+    need = w4.mx_workspace_bytes(T, 288, 8)
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN scales and codes
+    assert c.run(out=buf[:T], workspace=ws).data_ptr() == buf.data_ptr()
+    assert torch.equal(buf[:T], want) and (buf[T:] == 3).all()
+    assert (ws[need:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("T", [3, 20, 100])
+def test_infinity_and_nan_reach_only_their_rows(T):
+    for fmt in (4, 8):
+        c = Case("linear", T, 64, 416, "bf16", fmt)
+        want = c.run(fmt=fmt)
+        c.x[1, 40], c.x[2, 400] = float("inf"), float("nan")
+        got = c.run(fmt=fmt)
+        assert got[1].isnan().all() and got[2].isnan().all()
+        keep = [t for t in range(T) if t not in (1, 2)]
+        assert torch.equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_nan_scale_of_a_weight_reaches_only_its_row(T):
+    c = Case("linear", T, 48, 160, "bf16", 8)
+    want = c.run()
+    c.weights[0][1][17, 3] = 255
+    c.pw = w4.pack_mx(oracle.pack_fp4(c.weights[0][0]), c.weights[0][1], device=DEV)
+    got = c.run()
+    keep = [n for n in range(48) if n != 17]
+    assert got[:, 17].isnan().all() and torch.equal(got[:, keep], want[:, keep])
+
+
+def test_zero_activations_and_repeats():
+    for T in (2, 40, 100):
+        c = Case("add", T, 64, 256, "bf16", 4)
+        a = c.run(fmt=4)
+        for _ in range(3):
+            assert torch.equal(c.run(fmt=4), a)
+        c.x.zero_()
+        assert torch.equal(c.run(fmt=4), c.r)
+
+
+def test_weights_from_the_device_quantisation():
+    """quantize_mx's codes and scales are the canonical form of a weight matrix."""
+    g = torch.Generator().manual_seed(11)
+    wt = (0.05 * torch.randn(64, 672, generator=g)).bfloat16().to(DEV)
+    x = torch.randn(6, 672, generator=g).bfloat16().to(DEV)
+    q = w4.quantize_mx(wt, fmt=4)
+    y = w4.linear_mx(x, w4.pack_mx(q.codes, q.scales, device=DEV), fmt=8)
+    wv = exact64(w4.dequantize_mx(q, dtype=torch.bfloat16))
+    a = oracle.mx_value(*oracle.quantize_mx(exact64(x), 8), 8)
+    ref = a @ wv.T
+    tol = (np.abs(a) @ np.abs(wv).T) * 2.0 ** -11.9
+    assert np.all(np.abs(exact64(y) - ref) <= tol + np.abs(ref) * 2.0 ** -8)
+
+
+def test_binding_refusals():
+    c = Case("linear", 4, 64, 128, "fp16", 8)
+    q = w4.quantize_mx(c.x, fmt=8)
+    bad = [lambda: w4.linear_mx(c.x[:, :64].contiguous(), c.pw), lambda: w4.linear_mx(c.x.float(), c.pw),
+           lambda: w4.linear_mx(c.x.t(), c.pw), lambda: w4.linear_mx(c.x, c.pw, fmt=5), lambda: w4.linear_swiglu_mx(c.x, c.pw),
+           lambda: w4.linear_mx(c.x, c.pw, out=torch.empty(4, 64, device=DEV)), lambda: w4.linear_mx(q, c.pw, fmt=4),
+           lambda: w4.linear_mx(c.x, c.pw, dtype=torch.bfloat16), lambda: w4.linear_mx(q, c.pw, dtype=torch.float32),
+           lambda: w4.linear_mx(q, c.pw, workspace=q.workspace), lambda: w4.linear_add_mx(c.x, c.pw, c.x),
+           lambda: w4.linear_mx(c.x, w4.PackedMX(c.pw.w[:-1], c.pw.scales, 64, 128)),
+           lambda: w4.linear_mx(w4.MXTensor(q.workspace[:64], 4, 128, 8), c.pw),
+           lambda: w4.linear_mx(w4.quantize_mx(c.x[:, :96].contiguous()), c.pw)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(w4.W4Error):
+        w4.linear_mx(c.x, c.pw, out=c.x[:, :64].contiguous().new_empty(0).set_(c.x.untyped_storage(), 0, (4, 64)))
+    assert w4.linear_mx(c.x[:0], c.pw).shape == (0, 64)
+
+
+# ---- together, as a decoder layer's MLP uses them
+
+def mlp(x, residual, weight, gate_up, down, fmt):
+    q, h = w4.rmsnorm_mx(x, weight, fmt=fmt, residual=residual)
+    a = w4.linear_swiglu_mx(q, gate_up, dtype=x.dtype)
+    return w4.linear_add_mx(a, down, h, fmt=fmt), h
+
+
+def mlp_inputs(T, H, I, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    mk = lambda n, k: oracle.quantize_mx((0.1 * torch.randn(n, k, generator=g)).double().numpy(), 4)  # noqa: E731
+    ws = [mk(I, H), mk(I, H), mk(H, I)]
+    packed = [(oracle.pack_fp4(c), e) for c, e in ws]
+    x, r = (torch.randn(T, H, generator=g).to(dtype).to(DEV) for _ in range(2))
+    weight = (1 + 0.1 * torch.randn(H, generator=g)).to(dtype).to(DEV)
+    return ws, x, r, weight, w4.pack_mx_pair(packed[0], packed[1], device=DEV), w4.pack_mx(*packed[2], device=DEV)
+
+
+@pytest.mark.parametrize("T", [1, 6, 33, 150])
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_norm_and_products_together(T, fmt):
+    """Every stage against the oracle of that stage's own inputs."""
+    H, I = 288, 416
+    ws, x, r, weight, gate_up, down = mlp_inputs(T, H, I, torch.bfloat16)
+    q, h = w4.rmsnorm_mx(x, weight, fmt=fmt, residual=r)
+    a = w4.linear_swiglu_mx(q, gate_up, dtype=torch.bfloat16)
+    y = w4.linear_add_mx(a, down, h, fmt=fmt)
+    c = Case.__new__(Case)
+    c.op, c.T, c.N, c.K, c.fmt, c.dtype, c.weights = "swiglu", T, I, H, fmt, torch.bfloat16, ws[:2]
+    c.x = w4.dequantize_mx(q, dtype=torch.bfloat16)  # quantises to itself
+    assert torch.equal(w4.quantize_mx(c.x, fmt=fmt).codes, q.codes)
+    c.check(a)
+    c.op, c.N, c.K, c.weights, c.x, c.r = "add", H, I, ws[2:], a, h
+    c.check(y)
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 150])
+def test_captured_and_replayed(T):
+    ws, x, r, weight, gate_up, down = mlp_inputs(T, 256, 384, torch.float16, seed=T)
+    want, _ = mlp(x, r, weight, gate_up, down, 8)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got, _ = mlp(x, r, weight, gate_up, down, 8)
+    for rep in range(4):
+        x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(rep)).half())
+        want, _ = mlp(x, r, weight, gate_up, down, 8)
+        got.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), rep
+
+
+def test_graph_set_of_verify_widths():
+    graphs = w4.VerifyGraphs()
+    state = {}
+    for T in (1, 4, 40):
+        ws, x, r, weight, gate_up, down = mlp_inputs(T, 256, 384, torch.float16, seed=T)
+        out, h = torch.empty_like(x), torch.empty_like(x)
+        ws8 = torch.empty(w4.mx_workspace_bytes(T, 384, 8), dtype=torch.uint8, device=DEV)
+        act = torch.empty((T, 384), dtype=torch.float16, device=DEV)
+        state[T] = (x, r, weight, gate_up, down, out, h, ws8, act)
+
+    def step(T):
+        x, r, weight, gate_up, down, out, h, ws8, act = state[T]
+        q, _ = w4.rmsnorm_mx(x, weight, residual=r, residual_out=h, workspace=ws8)
+        w4.linear_swiglu_mx(q, gate_up, out=act)
+        w4.linear_add_mx(act, down, h, out=out, workspace=ws8)
+
+    for rep in range(3):
+        for T in (1, 4, 40):
+            x, r, weight, gate_up, down, out, *_ = state[T]
+            x.normal_()
+            torch.cuda.synchronize()
+            graphs.run(T, step)
+            graphs.stream.synchronize()
+            want, _ = mlp(x, r, weight, gate_up, down, 8)
+            assert torch.equal(out, want), (rep, T)
+    graphs.close()
+
+
+def test_two_streams_at_once():
+    cases = [Case("linear", T, 256, 1024, "fp16", 8, seed=T) for T in (2, 20, 100)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(10):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            got[i].append(c.run(stream=s))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(y, w) for y in g)
+
+
+def test_norm_feeds_the_a8_route():
+    """rmsnorm_a8's workspace in linear_a8(x=None) against the exact product of what it holds."""
+    from synth import make_weights
+    from gpu_util import canon
+    rng = np.random.default_rng(2)
+    wset = make_weights(rng, "w", 272, 704, 4, ("uniform", 6, 9), (0.005, 0.02))
+    pw = w4.pack_weight(*canon(wset), 4, device=DEV)
+    for T in (1, 130):
+        g = torch.Generator().manual_seed(T)
+        x, r = (torch.randn(T, 704, generator=g).half().to(DEV) for _ in range(2))
+        weight = (1 + 0.1 * torch.randn(704, generator=g)).half().to(DEV)
+        ws, _ = w4.rmsnorm_a8(x, weight, residual=r)
+        y = w4.linear_a8(None, pw, workspace=ws, T=T)
+        a = exact64(w4.dequantize_a8(ws, T, 704, dtype=torch.bfloat16))
+        ref = oracle.linear(a, *canon(wset), 4)
+        # a is rounded to bf16 (2^-9 relative each): rel L2 below 2^-8
+        assert oracle.rel_l2(exact64(y), ref) <= 2.0 ** -8

@@ -40,7 +40,12 @@ EXPORTS = (
     "w4_linear_route_bf16", "w4_linear_bf16_noalloc", "w4_graph_set_create", "w4_graph_set_begin",
     "w4_graph_set_end", "w4_graph_set_launch", "w4_graph_set_has", "w4_graph_set_destroy",
     "w4_a8_workspace_bytes", "w4_quantize_a8", "w4_linear_a8", "w4_linear_swiglu_a8", "w4_linear_add_a8",
+    "w4_dequantize_a8", "w4_mx_packed_bytes", "w4_mx_packed_scale_bytes", "w4_mx_workspace_bytes",
+    "w4_mx_repack", "w4_mx_repack_pair", "w4_quantize_mx", "w4_dequantize_mx", "w4_linear_mx",
+    "w4_linear_swiglu_mx", "w4_linear_add_mx", "w4_rmsnorm", "w4_rmsnorm_a8", "w4_rmsnorm_mx",
 )
+
+MXFP4, MXFP8 = 4, 8  # W4_MXFP4, W4_MXFP8: element formats of the microscaled calls
 
 
 class _Parent(ctypes.Structure):
@@ -129,6 +134,24 @@ def lib() -> ctypes.CDLL:
     L.w4_linear_swiglu_a8.restype = i
     L.w4_linear_add_a8.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, sz, vp]
     L.w4_linear_add_a8.restype = i
+    i64, f = ctypes.c_int64, ctypes.c_float
+    for name, args in (("w4_mx_packed_bytes", [i, i]), ("w4_mx_packed_scale_bytes", [i, i]),
+                       ("w4_mx_workspace_bytes", [i, i, i])):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = sz
+    for name, args in (
+            ("w4_mx_repack", [vp, vp, i, i, vp, vp]), ("w4_mx_repack_pair", [vp, vp, vp, vp, i, i, vp, vp]),
+            ("w4_quantize_mx", [vp, i64, i, i, i, i, vp, sz, vp]),
+            ("w4_dequantize_mx", [vp, sz, i, i, i, i, vp, vp]),
+            ("w4_dequantize_a8", [vp, sz, i, i, i, vp, vp]),
+            ("w4_linear_mx", [vp, vp, vp, i, i, i, i, i, vp, vp, sz, vp]),
+            ("w4_linear_swiglu_mx", [vp, vp, vp, i, i, i, i, i, vp, vp, sz, vp]),
+            ("w4_linear_add_mx", [vp, vp, vp, vp, i, i, i, i, i, vp, vp, sz, vp]),
+            ("w4_rmsnorm", [vp, i64, vp, vp, f, i, i, i, vp, vp, vp]),
+            ("w4_rmsnorm_a8", [vp, i64, vp, vp, f, i, i, i, vp, vp, sz, vp]),
+            ("w4_rmsnorm_mx", [vp, i64, vp, vp, f, i, i, i, i, vp, vp, sz, vp])):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = i
     _lib = L
     return L
 
@@ -557,6 +580,351 @@ def linear_swiglu_a8(x, pw: PackedWeight, out=None, workspace=None, stream=None,
 
 def linear_add_a8(x, pw: PackedWeight, residual, out=None, workspace=None, stream=None, T=None):
     return _a8_call(OP_ADD, x, pw, residual, out, workspace, stream, T)
+
+
+# ------------------------------------------------------------------ microscaled (MX) formats
+
+def mx_packed_bytes(N: int, K: int) -> int:
+    return int(lib().w4_mx_packed_bytes(N, K))
+
+
+def mx_packed_scale_bytes(N: int, K: int) -> int:
+    return int(lib().w4_mx_packed_scale_bytes(N, K))
+
+
+def mx_workspace_bytes(T: int, K: int, fmt: int) -> int:
+    return int(lib().w4_mx_workspace_bytes(T, K, fmt))
+
+
+@dataclasses.dataclass
+class PackedMX:
+    """MXFP4 weights in the device layout (torch tensors own the memory)."""
+    w: "object"        # torch.uint8 [mx_packed_bytes]
+    scales: "object"   # torch.uint8 [mx_packed_scale_bytes]
+    N: int             # output width (of each of gate/up for a pair)
+    K: int
+    pair: bool = False
+
+    @property
+    def nbytes_stream(self) -> int:
+        """Bytes one call streams: packed codes + scale bytes (padding included)."""
+        return self.w.numel() + self.scales.numel()
+
+
+@dataclasses.dataclass
+class MXTensor:
+    """Quantised activations [T, K]: a workspace of the MX calls and what it holds."""
+    workspace: "object"  # torch.uint8, >= mx_workspace_bytes(T, K, fmt)
+    T: int
+    K: int
+    fmt: int             # MXFP4 or MXFP8
+
+    @property
+    def codes(self):
+        """uint8 [T, K * fmt / 8] view: E4M3 codes, or E2M1 codes two to a byte (even column low)."""
+        n = self.K * self.fmt // 8
+        return self.workspace.view(-1)[:self.T * n].view(self.T, n)
+
+    @property
+    def scales(self):
+        """uint8 [T, K / 32] view of the scale bytes (rows 16 * ceil(K / 512) bytes apart)."""
+        off, stride = self.T * self.K * self.fmt // 8, (self.K + 511) // 512 * 16
+        return self.workspace.view(-1)[off:off + self.T * stride].view(self.T, stride)[:, :self.K // 32]
+
+
+def _mx_host(codes, scales) -> Tuple[np.ndarray, np.ndarray]:
+    """Canonical codes [N, K/2] and scale bytes [N, K/32] (arrays or tensors) as host arrays."""
+    pair = []
+    for a in (codes, scales):
+        a = np.ascontiguousarray(a.detach().cpu().numpy() if hasattr(a, "detach") else a)
+        if a.dtype != np.uint8 or a.ndim != 2:
+            raise ValueError("MX codes and scales are 2-D uint8")
+        pair.append(a)
+    if pair[0].shape[0] != pair[1].shape[0] or pair[0].shape[1] != 16 * pair[1].shape[1]:
+        raise ValueError(f"codes {pair[0].shape} and scales {pair[1].shape} do not belong together")
+    return pair[0], pair[1]
+
+
+def repack_mx(codes, scales) -> Tuple[np.ndarray, np.ndarray]:
+    """Canonical MXFP4 weights -> packed (codes, scales) host arrays."""
+    c, e = _mx_host(codes, scales)
+    N, K = c.shape[0], c.shape[1] * 2
+    w, so = np.empty(mx_packed_bytes(N, K), np.uint8), np.empty(mx_packed_scale_bytes(N, K), np.uint8)
+    _check(lib().w4_mx_repack(_ptr(c), _ptr(e), N, K, _ptr(w), _ptr(so)), "w4_mx_repack")
+    return w, so
+
+
+def repack_mx_pair(gate, up) -> Tuple[np.ndarray, np.ndarray]:
+    """gate, up = canonical (codes, scales) -> the interleaved pair layout."""
+    (gc, gs), (uc, us) = _mx_host(*gate), _mx_host(*up)
+    if gc.shape != uc.shape:
+        raise ValueError("gate and up differ in shape")
+    N, K = gc.shape[0], gc.shape[1] * 2
+    w, so = np.empty(mx_packed_bytes(2 * N, K), np.uint8), np.empty(mx_packed_scale_bytes(2 * N, K), np.uint8)
+    _check(lib().w4_mx_repack_pair(_ptr(gc), _ptr(gs), _ptr(uc), _ptr(us), N, K, _ptr(w), _ptr(so)),
+           "w4_mx_repack_pair")
+    return w, so
+
+
+def pack_mx(codes, scales, device="cuda") -> PackedMX:
+    """Canonical MXFP4 weights (codes [N, K/2], scale bytes [N, K/32]) onto the device."""
+    import torch
+    w, e = repack_mx(codes, scales)
+    return PackedMX(torch.from_numpy(w).to(device), torch.from_numpy(e).to(device), codes.shape[0],
+                    codes.shape[1] * 2)
+
+
+def pack_mx_pair(gate, up, device="cuda") -> PackedMX:
+    """A gate/up pair, each canonical (codes, scales), onto the device for linear_swiglu_mx."""
+    import torch
+    w, e = repack_mx_pair(gate, up)
+    return PackedMX(torch.from_numpy(w).to(device), torch.from_numpy(e).to(device), gate[0].shape[0],
+                    gate[0].shape[1] * 2, True)
+
+
+def _on(device, stream, call):
+    """call(raw stream) with `device` current and `stream` (default: the device's current one) the
+    current stream, so that what the call allocates belongs to the stream that uses it."""
+    import torch
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return call(torch.cuda.current_stream(device).cuda_stream)
+        stream = torch.cuda.current_stream(device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _dtype16(dtype) -> int:
+    import torch
+    if dtype is torch.float16:
+        return 0
+    if dtype is torch.bfloat16:
+        return 1
+    raise ValueError(f"expected float16 or bfloat16, got {dtype}")
+
+
+def _check_rows(x, name: str) -> None:
+    """x: CUDA [T, K] in 16 bits, columns contiguous (rows may be further apart than K)."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA tensor of shape [T, K]")
+    _dtype16(x.dtype)
+    if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+
+
+def _row_stride(x) -> int:
+    return x.stride(0) if x.shape[0] > 1 else (x.shape[1] + 7) // 8 * 8
+
+
+def _check_fmt(fmt: int) -> None:
+    if fmt not in (MXFP4, MXFP8):
+        raise ValueError(f"fmt must be MXFP4 ({MXFP4}) or MXFP8 ({MXFP8}), got {fmt!r}")
+
+
+def _bytes_on(workspace, need: int, device):
+    """`workspace`, checked, or a new one of `need` bytes."""
+    import torch
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device or workspace.dtype != torch.uint8 or \
+            not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of >= {need} bytes on {device}")
+    return workspace
+
+
+def _mx_need(T: int, K: int, fmt: int) -> int:
+    return T * (K * fmt // 8 + (K + 511) // 512 * 16)
+
+
+def _check_mx_tensor(q) -> None:
+    import torch
+    _check_fmt(q.fmt)
+    if not isinstance(q.workspace, torch.Tensor) or not q.workspace.is_cuda:
+        raise ValueError("the quantised activations must be on a GPU")
+    _bytes_on(q.workspace, _mx_need(q.T, q.K, q.fmt), q.workspace.device)
+
+
+def quantize_mx(x, fmt: int = MXFP4, workspace=None, stream=None) -> MXTensor:
+    """x (fp16 or bf16 [T, K], K a multiple of 32) -> MXTensor, via ``w4_quantize_mx``."""
+    _check_rows(x, "x")
+    _check_fmt(fmt)
+    T, K = x.shape
+    if K % 32:
+        raise ValueError(f"K must be a multiple of 32, got {K}")
+
+    def call(raw):
+        ws = _bytes_on(workspace, _mx_need(T, K, fmt), x.device)
+        _check(lib().w4_quantize_mx(x.data_ptr(), _row_stride(x), T, K, fmt, _dtype16(x.dtype), ws.data_ptr(),
+                                    ws.numel(), raw), "w4_quantize_mx")
+        return MXTensor(ws, T, K, fmt)
+    return _on(x.device, stream, call)
+
+
+def dequantize_mx(q: MXTensor, dtype=None, out=None, stream=None):
+    """MXTensor -> 16-bit [T, K] (dtype: torch.float16 unless given or `out` decides)."""
+    _check_mx_tensor(q)
+    return _dequantize(lambda *a: lib().w4_dequantize_mx(q.workspace.data_ptr(), q.workspace.numel(), q.T, q.K,
+                                                         q.fmt, *a), "w4_dequantize_mx", q.workspace, q.T, q.K,
+                       dtype, out, stream)
+
+
+def dequantize_a8(workspace, T: int, K: int, dtype=None, out=None, stream=None):
+    """A workspace of quantize_a8 or rmsnorm_a8 -> 16-bit [T, K]."""
+    import torch
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    nbytes = workspace.numel() * workspace.element_size()
+    return _dequantize(lambda *a: lib().w4_dequantize_a8(workspace.data_ptr(), nbytes, T, K, *a),
+                       "w4_dequantize_a8", workspace, T, K, dtype, out, stream)
+
+
+def _dequantize(fn, where, workspace, T, K, dtype, out, stream):
+    import torch
+    device = workspace.device
+    if dtype is None:
+        dtype = torch.float16 if out is None else out.dtype
+    code = _dtype16(dtype)
+
+    def call(raw):
+        if out is None:
+            o = torch.empty((T, K), dtype=dtype, device=device)
+        else:
+            o = out
+            _check_tensor(o, "out", (T, K), dtype, device)
+        _check(fn(code, o.data_ptr(), raw), where)
+        return o
+    return _on(device, stream, call)
+
+
+def _linear_mx(op: int, x, pw: PackedMX, residual, fmt, out, workspace, dtype, stream):
+    import torch
+    if (op == OP_SWIGLU) != pw.pair:
+        raise ValueError("linear_swiglu_mx takes a gate/up pair from pack_mx_pair; the others a single matrix")
+    if isinstance(x, MXTensor):
+        _check_mx_tensor(x)
+        if x.K != pw.K:
+            raise ValueError(f"the quantised activations have K = {x.K}, the weights {pw.K}")
+        if workspace is not None or fmt not in (None, x.fmt):
+            raise ValueError("quantised activations bring their own workspace and format")
+        T, fmt, workspace, device = x.T, x.fmt, x.workspace, x.workspace.device
+        if dtype is None:
+            dtype = out.dtype if out is not None else residual.dtype if residual is not None else torch.float16
+        xp = None
+    else:
+        if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
+            raise ValueError("x must be a CUDA tensor of shape [T, K] or an MXTensor")
+        _check_tensor(x, "x", (x.shape[0], pw.K), x.dtype, x.device)
+        if dtype not in (None, x.dtype):
+            raise ValueError("the output has the activations' dtype")
+        fmt = MXFP8 if fmt is None else fmt
+        _check_fmt(fmt)
+        T, dtype, device, xp = x.shape[0], x.dtype, x.device, x.data_ptr()
+    code = _dtype16(dtype)
+    rows, KB = (2 * pw.N if pw.pair else pw.N) // 16, (pw.K + 127) // 128
+    _check_tensor(pw.w, "packed codes", (rows * KB * 1024,), torch.uint8, device)
+    _check_tensor(pw.scales, "packed scales", (rows * KB * 64,), torch.uint8, device)
+    if op == OP_ADD:
+        _check_tensor(residual, "residual", (T, pw.N), dtype, device)
+
+    def call(raw):
+        if out is None:
+            o = torch.empty((T, pw.N), dtype=dtype, device=device)
+        else:
+            o = out
+            _check_tensor(o, "out", (T, pw.N), dtype, device)
+        ws = _bytes_on(workspace, _mx_need(T, pw.K, fmt), device)
+        L, head = lib(), (xp, pw.w.data_ptr(), pw.scales.data_ptr())
+        tail = (T, pw.N, pw.K, fmt, code, o.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+        if op == OP_ADD:
+            _check(L.w4_linear_add_mx(*head, residual.data_ptr(), *tail), "w4_linear_add_mx")
+        elif op == OP_SWIGLU:
+            _check(L.w4_linear_swiglu_mx(*head, *tail), "w4_linear_swiglu_mx")
+        else:
+            _check(L.w4_linear_mx(*head, *tail), "w4_linear_mx")
+        return o
+    return _on(device, stream, call)
+
+
+def linear_mx(x, pw: PackedMX, fmt=None, out=None, workspace=None, dtype=None, stream=None):
+    """out[T, N] = x . W^T with MXFP4 weights, via ``w4_linear_mx``.  x: fp16 or bf16 [T, K], quantised
+    to fmt (MXFP8 unless given) inside the call, or an MXTensor (from quantize_mx or rmsnorm_mx; then
+    dtype, torch.float16 unless given or `out` / the residual decides, is the output's type)."""
+    return _linear_mx(OP_LINEAR, x, pw, None, fmt, out, workspace, dtype, stream)
+
+
+def linear_swiglu_mx(x, pw: PackedMX, fmt=None, out=None, workspace=None, dtype=None, stream=None):
+    """out[T, N] = silu(x . Wg^T) * (x . Wu^T), pw from pack_mx_pair; otherwise as linear_mx."""
+    return _linear_mx(OP_SWIGLU, x, pw, None, fmt, out, workspace, dtype, stream)
+
+
+def linear_add_mx(x, pw: PackedMX, residual, fmt=None, out=None, workspace=None, dtype=None, stream=None):
+    """out[T, N] = x . W^T + residual (out may be residual); otherwise as linear_mx."""
+    return _linear_mx(OP_ADD, x, pw, residual, fmt, out, workspace, dtype, stream)
+
+
+# ------------------------------------------------------------------ RMS norm
+
+def _rmsnorm(fn, where, x, weight, eps, residual, residual_out, k_multiple, stream, buffer):
+    """Shared checks; buffer() gives (the C call's trailing arguments, the result)."""
+    import torch
+    _check_rows(x, "x")
+    T, K = x.shape
+    if K < 1 or K % k_multiple:
+        raise ValueError(f"K must be a positive multiple of {k_multiple}, got {K}")
+    _check_tensor(weight, "weight", (K,), x.dtype, x.device)
+    if residual is not None:
+        _check_tensor(residual, "residual", (T, K), x.dtype, x.device)
+        if residual_out is not None:
+            _check_tensor(residual_out, "residual_out", (T, K), x.dtype, x.device)
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+
+    def call(raw):
+        h = residual_out
+        if residual is not None and h is None:
+            h = torch.empty((T, K), dtype=x.dtype, device=x.device)
+        mid, tail, result = buffer(T, K)
+        _check(fn()(x.data_ptr(), max(_row_stride(x), K) if T > 1 else K, _dptr(residual), weight.data_ptr(), eps, T,
+                    K, *mid, _dtype16(x.dtype), _dptr(h), *tail, raw), where)
+        return result, h
+    return _on(x.device, stream, call)
+
+
+def rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out=None, stream=None):
+    """(y, h): h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight per row of x [T, K] (fp16 or
+    bf16, rows may be strided), via ``w4_rmsnorm``.  Without a residual h is None; residual_out may
+    be residual (or a contiguous x), out either too."""
+    import torch
+
+    def buffer(T, K):
+        o = torch.empty((T, K), dtype=x.dtype, device=x.device) if out is None else out
+        _check_tensor(o, "out", (T, K), x.dtype, x.device)
+        return (), (o.data_ptr(),), o
+    return _rmsnorm(lambda: lib().w4_rmsnorm, "w4_rmsnorm", x, weight, eps, residual, residual_out, 1, stream, buffer)
+
+
+def rmsnorm_a8(x, weight, eps: float = 1e-6, residual=None, residual_out=None, workspace=None, stream=None):
+    """As rmsnorm with y quantised for the A8 calls: (workspace, h); linear_a8(None, pw,
+    workspace=workspace, T=T) reads it.  K a multiple of 64."""
+    def buffer(T, K):
+        ws = _a8_workspace(workspace, T, K, x.device)
+        return (), (ws.data_ptr(), ws.numel() * ws.element_size()), ws
+    return _rmsnorm(lambda: lib().w4_rmsnorm_a8, "w4_rmsnorm_a8", x, weight, eps, residual, residual_out, 64, stream,
+                    buffer)
+
+
+def rmsnorm_mx(x, weight, fmt: int = MXFP8, eps: float = 1e-6, residual=None, residual_out=None, workspace=None,
+               stream=None):
+    """As rmsnorm with y quantised to fmt: (MXTensor, h); linear_mx takes the MXTensor.  K a multiple
+    of 32."""
+    _check_fmt(fmt)
+
+    def buffer(T, K):
+        ws = _bytes_on(workspace, _mx_need(T, K, fmt), x.device)
+        return (fmt,), (ws.data_ptr(), ws.numel()), MXTensor(ws, T, K, fmt)
+    return _rmsnorm(lambda: lib().w4_rmsnorm_mx, "w4_rmsnorm_mx", x, weight, eps, residual, residual_out, 32, stream,
+                    buffer)
 
 
 # ------------------------------------------------------------------ per-verify-width graphs

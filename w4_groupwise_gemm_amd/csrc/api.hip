@@ -18,6 +18,7 @@
 #include "device.h"
 #include "kernels.h"
 #include "layout.h"
+#include "mx.h"
 
 namespace {
 
@@ -133,6 +134,12 @@ int device_check() {
   }
   return v == 1 ? W4_OK : W4_ERR_DEVICE;
 }
+
+}  // namespace
+
+int w4::device_status() { return device_check(); }
+
+namespace {
 
 // Boundaries from route sweeps on this chip (every route timed at the same T, cold weights, at
 // the decode, batched-decode, SwiGLU-pair and 5120-row prefill shapes and at 5120-row matrices

@@ -1,0 +1,233 @@
+// C ABI of the MX formats and the RMS norm: argument validation and launches.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <initializer_list>
+
+#include "../../include/w4gemm.h"
+#include "mx.h"
+
+namespace {
+
+constexpr int kMaxDim = 1 << 24;
+constexpr size_t kLimit = (size_t)1 << 31;  // tensors of the products stay below 2 GiB
+
+struct Range {
+  uintptr_t lo, hi;
+};
+Range span(const void* p, size_t n) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return {b, b + (p ? n : 0)};
+}
+bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool dims_ok(int T, int K) { return T >= 0 && K > 0 && T <= kMaxDim && K <= kMaxDim; }
+bool mx_dims_ok(int T, int K) { return dims_ok(T, K) && K % w4::kMxBlock == 0; }
+bool fmt_ok(int fmt) { return fmt == W4_MXFP4 || fmt == W4_MXFP8; }
+bool dtype_ok(int dtype) { return dtype == W4_FP16 || dtype == W4_BF16; }
+// kernels with one thread per 32 columns: the launch's thread count is 32 bits
+bool grid_ok(int T, int K) { return (uint64_t)T * (K / 32) < 0xFFFFFF00u; }
+
+size_t a8_bytes(int T, int K) {
+  return ((size_t)T * K + 15) / 16 * 16 + (size_t)w4layout::num_kblocks(K) * T * 2 * sizeof(float);
+}
+
+// Bytes from the first element of row 0 to the end of row T - 1, rows ldx elements apart.
+size_t strided_bytes(int T, int K, int64_t ldx) { return ((size_t)(T - 1) * ldx + K) * 2; }
+
+// A workspace: present, aligned, large enough, overlapping none of `others`.
+int check_ws(const void* ws, size_t bytes, size_t need, std::initializer_list<Range> others) {
+  if (!ws) return W4_ERR_INVALID_ARG;
+  if (!aligned16(ws)) return W4_ERR_MISALIGNED;
+  if (bytes < need) return W4_ERR_INVALID_ARG;
+  for (const Range& r : others)
+    if (overlap(span(ws, need), r)) return W4_ERR_ALIAS;
+  return W4_OK;
+}
+
+int launched(hipError_t e) { return e == hipSuccess ? W4_OK : W4_ERR_LAUNCH; }
+
+int run_linear_mx(int op, const uint16_t* x, const void* w, const uint8_t* scales, const uint16_t* res, int T, int N,
+                  int K, int fmt, int dtype, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!fmt_ok(fmt) || !dtype_ok(dtype)) return W4_ERR_UNSUPPORTED;
+  if (!mx_dims_ok(T, K) || N <= 0 || N > kMaxDim || N % w4layout::kRowTile) return W4_ERR_INVALID_ARG;
+  if (T == 0) return W4_OK;
+  if (!w || !scales || !out || (op == W4_OP_ADD && !res)) return W4_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(scales) || !aligned16(out) || !aligned16(res))
+    return W4_ERR_MISALIGNED;
+  const int rows = op == W4_OP_SWIGLU ? 2 * N : N;
+  const size_t wb = w4_mx_packed_bytes(rows, K), sb = w4_mx_packed_scale_bytes(rows, K);
+  const size_t xb = (size_t)T * K * 2, ob = (size_t)T * N * 2;
+  if (xb >= kLimit || ob >= kLimit || wb >= kLimit) return W4_ERR_UNSUPPORTED;
+  const Range ro = span(out, ob), rr = span(res, ob);
+  if (overlap(ro, span(x, xb)) || overlap(ro, span(w, wb)) || overlap(ro, span(scales, sb)) ||
+      (res != out && overlap(ro, rr)))
+    return W4_ERR_ALIAS;
+  int st = check_ws(ws, ws_bytes, w4::mx_workspace_bytes(T, K, fmt),
+                    {span(x, xb), ro, rr, span(w, wb), span(scales, sb)});
+  if (st != W4_OK) return st;
+  st = w4::device_status();
+  if (st != W4_OK) return st;
+  const hipStream_t hs = static_cast<hipStream_t>(stream);
+  uint8_t* codes = static_cast<uint8_t*>(ws);
+  uint8_t* xs = codes + w4::mx_scale_offset(T, K, fmt);
+  const bool bf16 = dtype == W4_BF16;
+  if (x && w4::launch_mx_quant(x, K, T, K, bf16, fmt, codes, xs, hs) != hipSuccess) return W4_ERR_LAUNCH;
+  w4::MxArgs a;
+  a.xq = codes;
+  a.xs = xs;
+  a.x = nullptr;
+  a.w = static_cast<const uint8_t*>(w);
+  a.ws = scales;
+  a.res = res;
+  a.out = out;
+  a.T = T;
+  a.rows = rows;
+  a.K = K;
+  a.KB = w4layout::num_kblocks(K);
+  a.ldo = N;
+  const int epi = op == W4_OP_SWIGLU ? w4dev::EPI_SWIGLU : op == W4_OP_ADD ? w4dev::EPI_ADD : w4dev::EPI_STORE;
+  return launched(w4::launch_mx_stream(epi, bf16, fmt, a, hs));
+}
+
+// kind: one of w4::NORM_*.  need: bytes of the workspace (0: the 16-bit output `out` instead).
+int run_rmsnorm(int kind, const uint16_t* x, int64_t ldx, const uint16_t* res, const uint16_t* weight, float eps,
+                int T, int K, int k_multiple, int dtype, uint16_t* res_out, uint16_t* out, void* ws, size_t ws_bytes,
+                size_t need, size_t scale_offset, void* stream) {
+  if (!dtype_ok(dtype)) return W4_ERR_UNSUPPORTED;
+  if (!dims_ok(T, K) || K % k_multiple || ldx < K || ldx > ((int64_t)1 << 40)) return W4_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || std::isinf(eps)) return W4_ERR_INVALID_ARG;
+  if ((res == nullptr) != (res_out == nullptr)) return W4_ERR_INVALID_ARG;
+  if (T == 0) return W4_OK;
+  if (!x || !weight || (need == 0 && !out)) return W4_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(res) || !aligned16(weight) || !aligned16(res_out) || !aligned16(out))
+    return W4_ERR_MISALIGNED;
+  const size_t nb = (size_t)T * K * 2;
+  const Range rx = span(x, strided_bytes(T, K, ldx)), rr = span(res, nb), rw = span(weight, (size_t)K * 2);
+  const Range rh = span(res_out, nb), ro = span(out, nb);
+  // an output may be one of the row inputs exactly: every element is read before it is written
+  auto clash = [&](const void* p, Range r) {
+    return (overlap(r, rx) && !(p == x && ldx == K)) || (overlap(r, rr) && p != res) || overlap(r, rw);
+  };
+  if (clash(res_out, rh) || clash(out, ro) || overlap(rh, ro)) return W4_ERR_ALIAS;
+  if (need) {
+    const int st = check_ws(ws, ws_bytes, need, {rx, rr, rw, rh});
+    if (st != W4_OK) return st;
+  }
+  const int st = w4::device_status();
+  if (st != W4_OK) return st;
+  w4::NormArgs a;
+  a.x = x;
+  a.res = res;
+  a.weight = weight;
+  a.res_out = res_out;
+  a.out = out;
+  a.codes = ws;
+  a.scales = need ? static_cast<char*>(ws) + scale_offset : nullptr;
+  a.ldx = ldx;
+  a.eps = eps;
+  a.T = T;
+  a.K = K;
+  return launched(w4::launch_norm(kind, dtype == W4_BF16, a, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" size_t w4_mx_workspace_bytes(int T, int K, int fmt) {
+  return mx_dims_ok(T, K) && fmt_ok(fmt) ? w4::mx_workspace_bytes(T, K, fmt) : 0;
+}
+
+extern "C" int w4_quantize_mx(const uint16_t* x, int64_t ldx, int T, int K, int fmt, int dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!fmt_ok(fmt) || !dtype_ok(dtype)) return W4_ERR_UNSUPPORTED;
+  if (!mx_dims_ok(T, K) || ldx < K || ldx % 8 || ldx > ((int64_t)1 << 40)) return W4_ERR_INVALID_ARG;
+  if (T == 0) return W4_OK;
+  if (!grid_ok(T, K)) return W4_ERR_UNSUPPORTED;
+  if (!x) return W4_ERR_INVALID_ARG;
+  if (!aligned16(x)) return W4_ERR_MISALIGNED;
+  int st = check_ws(workspace, workspace_bytes, w4::mx_workspace_bytes(T, K, fmt), {span(x, strided_bytes(T, K, ldx))});
+  if (st != W4_OK) return st;
+  st = w4::device_status();
+  if (st != W4_OK) return st;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  return launched(w4::launch_mx_quant(x, ldx, T, K, dtype == W4_BF16, fmt, codes,
+                                      codes + w4::mx_scale_offset(T, K, fmt), static_cast<hipStream_t>(stream)));
+}
+
+extern "C" int w4_dequantize_mx(const void* workspace, size_t workspace_bytes, int T, int K, int fmt, int dtype,
+                                uint16_t* out, void* stream) {
+  if (!fmt_ok(fmt) || !dtype_ok(dtype)) return W4_ERR_UNSUPPORTED;
+  if (!mx_dims_ok(T, K)) return W4_ERR_INVALID_ARG;
+  if (T == 0) return W4_OK;
+  if (!grid_ok(T, K)) return W4_ERR_UNSUPPORTED;
+  if (!out) return W4_ERR_INVALID_ARG;
+  if (!aligned16(out)) return W4_ERR_MISALIGNED;
+  int st = check_ws(workspace, workspace_bytes, w4::mx_workspace_bytes(T, K, fmt), {span(out, (size_t)T * K * 2)});
+  if (st != W4_OK) return st;
+  st = w4::device_status();
+  if (st != W4_OK) return st;
+  const uint8_t* codes = static_cast<const uint8_t*>(workspace);
+  return launched(w4::launch_mx_dequant(codes, codes + w4::mx_scale_offset(T, K, fmt), T, K, dtype == W4_BF16, fmt,
+                                        out, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" int w4_dequantize_a8(const void* workspace, size_t workspace_bytes, int T, int K, int dtype, uint16_t* out,
+                                void* stream) {
+  if (!dtype_ok(dtype)) return W4_ERR_UNSUPPORTED;
+  if (!dims_ok(T, K) || K % 64) return W4_ERR_INVALID_ARG;
+  if (T == 0) return W4_OK;
+  if (!grid_ok(T, K)) return W4_ERR_UNSUPPORTED;
+  if (!out) return W4_ERR_INVALID_ARG;
+  if (!aligned16(out)) return W4_ERR_MISALIGNED;
+  int st = check_ws(workspace, workspace_bytes, a8_bytes(T, K), {span(out, (size_t)T * K * 2)});
+  if (st != W4_OK) return st;
+  st = w4::device_status();
+  if (st != W4_OK) return st;
+  const char* ws = static_cast<const char*>(workspace);
+  return launched(w4::launch_a8_dequant(reinterpret_cast<const int8_t*>(ws),
+                                        reinterpret_cast<const float*>(ws + ((size_t)T * K + 15) / 16 * 16), T, K,
+                                        dtype == W4_BF16, out, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" int w4_linear_mx(const uint16_t* x, const void* w, const uint8_t* scales, int T, int N, int K, int fmt,
+                            int dtype, uint16_t* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_linear_mx(W4_OP_LINEAR, x, w, scales, nullptr, T, N, K, fmt, dtype, out, workspace, workspace_bytes,
+                       stream);
+}
+
+extern "C" int w4_linear_swiglu_mx(const uint16_t* x, const void* w_pair, const uint8_t* scales_pair, int T, int N,
+                                   int K, int fmt, int dtype, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  return run_linear_mx(W4_OP_SWIGLU, x, w_pair, scales_pair, nullptr, T, N, K, fmt, dtype, out, workspace,
+                       workspace_bytes, stream);
+}
+
+extern "C" int w4_linear_add_mx(const uint16_t* x, const void* w, const uint8_t* scales, const uint16_t* residual,
+                                int T, int N, int K, int fmt, int dtype, uint16_t* out, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  return run_linear_mx(W4_OP_ADD, x, w, scales, residual, T, N, K, fmt, dtype, out, workspace, workspace_bytes,
+                       stream);
+}
+
+extern "C" int w4_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* residual, const uint16_t* weight, float eps,
+                          int T, int K, int dtype, uint16_t* residual_out, uint16_t* out, void* stream) {
+  return run_rmsnorm(w4::NORM_16, x, ldx, residual, weight, eps, T, K, 1, dtype, residual_out, out, nullptr, 0, 0, 0,
+                     stream);
+}
+
+extern "C" int w4_rmsnorm_a8(const uint16_t* x, int64_t ldx, const uint16_t* residual, const uint16_t* weight,
+                             float eps, int T, int K, int dtype, uint16_t* residual_out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return run_rmsnorm(w4::NORM_A8, x, ldx, residual, weight, eps, T, K, 64, dtype, residual_out, nullptr, workspace,
+                     workspace_bytes, dims_ok(T, K) ? a8_bytes(T, K) : 1, ((size_t)T * K + 15) / 16 * 16, stream);
+}
+
+extern "C" int w4_rmsnorm_mx(const uint16_t* x, int64_t ldx, const uint16_t* residual, const uint16_t* weight,
+                             float eps, int T, int K, int fmt, int dtype, uint16_t* residual_out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!fmt_ok(fmt)) return W4_ERR_UNSUPPORTED;
+  return run_rmsnorm(fmt == W4_MXFP4 ? w4::NORM_MX4 : w4::NORM_MX8, x, ldx, residual, weight, eps, T, K,
+                     w4::kMxBlock, dtype, residual_out, nullptr, workspace, workspace_bytes,
+                     dims_ok(T, K) ? w4::mx_workspace_bytes(T, K, fmt) : 1, w4::mx_scale_offset(T, K, fmt), stream);
+}
