@@ -253,9 +253,9 @@ int w4_linear_grouped(const uint16_t* x, const w4_parent* parents, int nparents,
  *
  * Weights are MXFP4.  Canonical (host) form: codes [N][K/2], scale bytes [N][K/32].  Packed (device)
  * form, row tiles of 16 rows and k-blocks of 128 columns, KB = ceil(K / 128): codes
- * [N/16][KB][64 lanes][16 bytes] and scale bytes [N/16][KB][64 lanes]; lane l holds row l % 16, columns
- * 32 (l / 16) .. + 31 of the k-block, in canonical order.  Columns past K are zeros.  A SwiGLU pair
- * interleaves the row tiles of gate and up as w4_repack_pair does.
+ * [N/16][KB][64 lanes][16 bytes], lane l holding row l % 16, columns 32 (l / 16) .. + 31 of the k-block,
+ * in canonical order; scale bytes [N/16][KB][16 rows][4 blocks].  Columns past K are zeros.  A SwiGLU
+ * pair interleaves the row tiles of gate and up as w4_repack_pair does.
  *
  * Activations are quantised to either format into a workspace: codes row-major [T][K * fmt / 8], then
  * scale bytes [T][S], S = 16 * ceil(K / 512) (bytes past K / 32 are 0).  With MXFP4 and K a multiple of

@@ -110,14 +110,14 @@ def _spec_pack(tiles, K):
     """Packed bytes of a list of (codes [16, K/2], scales [16, K/32]) row tiles, from the header."""
     KB = -(-K // 128)
     w = np.zeros((len(tiles), KB, 64, 16), np.uint8)
-    s = np.zeros((len(tiles), KB, 64), np.uint8)
+    s = np.zeros((len(tiles), KB, 16, 4), np.uint8)
     for i, (c, e) in enumerate(tiles):
         for kb in range(KB):
             for lane in range(64):
                 k = 128 * kb + 32 * (lane // 16)
                 if k < K:
                     w[i, kb, lane] = c[lane % 16, k // 2:k // 2 + 16]
-                    s[i, kb, lane] = e[lane % 16, k // 32]
+                    s[i, kb, lane % 16, lane // 16] = e[lane % 16, k // 32]
     return w.reshape(-1), s.reshape(-1)
 
 

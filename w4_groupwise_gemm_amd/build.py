@@ -25,7 +25,7 @@ STREAM_PARTS = [("stream.hip", [f"-DW4_STREAM_BITS={b}", f"-DW4_STREAM_EPI={e}"]
 NARROW_PARTS = [("narrow.hip", [f"-DW4_NARROW_BITS={b}"], f"narrow_b{b}.o") for b in (4, 5)]
 REGRING_PARTS = [("regring.hip", [f"-DW4_REGRING_BITS={b}"], f"regring_b{b}.o") for b in (4, 5)]
 SOURCES = STREAM_PARTS + NARROW_PARTS + REGRING_PARTS + ["api.hip", "splitk.hip", "wide.hip", "bf16.hip", "a8.hip", "repack.cpp", "graphs.cpp",
-                                                           "mx_api.hip", "mx_quant.hip", "mx_stream.hip", "norm.hip", "mx_repack.cpp"]
+                                                           "mx_api.hip", "mx_quant.hip", "mx_stream.hip", "mx_wide.hip", "norm.hip", "mx_repack.cpp"]
 PROBE_SOURCES = ["probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc" if os.path.exists("/opt/rocm/bin/hipcc") else "hipcc")

@@ -22,14 +22,15 @@ inline size_t mx_workspace_bytes(int T, int K, int fmt) {
 }
 
 struct MxArgs {
-  const uint8_t* xq;  // activation codes, row-major (NULL: quantise `x`)
+  const uint8_t* xq;  // activation codes, row-major
   const uint8_t* xs;  // activation scales, rows of mx_scale_stride(K) bytes
-  const uint16_t* x;  // [T][K] fp16 / bf16 bits
+  const uint16_t* x;  // [T][K] fp16 / bf16 bits to quantise on the way, or NULL: xq and xs hold them
   const uint8_t* w;   // packed codes: [rows / 16][KB][64 lanes][16 bytes]
-  const uint8_t* ws;  // packed scales: [rows / 16][KB][64 lanes]
+  const uint8_t* ws;  // packed scales: [rows / 16][KB][16 rows][4 blocks]
   const uint16_t* res;
   uint16_t* out;
   int T, rows, K, KB, ldo;
+  int epi, bf16;      // EPI_*; element type of x, res and out
 };
 
 struct NormArgs {
@@ -54,7 +55,10 @@ hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int T,
 hipError_t launch_a8_dequant(const int8_t* codes, const float* scales, int T, int K, bool bf16, uint16_t* out,
                              hipStream_t stream);
 hipError_t launch_norm(int kind, bool bf16, const NormArgs& a, hipStream_t stream);
-hipError_t launch_mx_stream(int epi, bool bf16, int fmt, const MxArgs& a, hipStream_t stream);
+// Whether the streaming kernel holds T x K activations in LDS; it then also quantises them itself.
+bool mx_stream_fits(int T, int K, int fmt);
+hipError_t launch_mx_stream(int fmt, const MxArgs& a, hipStream_t stream);
+hipError_t launch_mx_wide(int fmt, const MxArgs& a, hipStream_t stream);
 
 // Status of the current device (W4_OK when it is a gfx950); defined in api.hip.
 int device_status();
@@ -204,22 +208,39 @@ __device__ __forceinline__ f32x4 mfma_mx16(u32x4 w, uint32_t sw, const uint32_t 
   }
 }
 
-// Epilogue of 4 consecutive output columns n .. n + 3 of token t, one rounding from fp32.
-template <int EPI, bool BF>
+// Same with 32 x 32 x 64 steps, block half `u` of 128 columns: lane l holds row / column l % 32, scale
+// block 2 u + l / 32 (E4M3 operands as columns 16 (l / 32) .. + 15 and 32 + 16 (l / 32) .. + 15 of the 64);
+// the scale registers hold the bytes of blocks l / 32 and 2 + l / 32 in bytes 0 and 2.  It then holds D
+// rows 8 (v / 4) + 4 (l / 32) + v % 4, column l % 32, v = 0 .. 15.
+template <int FMT, int U>
+__device__ __forceinline__ f32x16 mfma_mx32(u32x4 w, uint32_t sw, const uint32_t (&x)[FMT], uint32_t sx, f32x16 c) {
+  const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+  if constexpr (FMT == 4) {
+    const i32x8 b = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 2 * U, (int)sw, 2 * U, (int)sx);
+  } else {
+    const i32x8 b = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)x[4], (int)x[5], (int)x[6], (int)x[7]};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 0, 2 * U, (int)sw, 2 * U, (int)sx);
+  }
+}
+
+// Epilogue of 4 consecutive output columns n .. n + 3 of token t, one rounding from fp32.  The
+// operation and the 16-bit type are the same for the whole launch.
 __device__ __forceinline__ void store_quad_mx(const w4::MxArgs& a, int t, int n, f32x4 v, f32x4 up) {
   const size_t off = (size_t)t * a.ldo + n;
-  float y[4];
-  if constexpr (EPI == EPI_ADD) {
+  if (a.epi == EPI_ADD) {
     const u32x2 r = *reinterpret_cast<const u32x2*>(a.res + off);
-    y[0] = v[0] + lo16<BF>(r[0]);
-    y[1] = v[1] + hi16<BF>(r[0]);
-    y[2] = v[2] + lo16<BF>(r[1]);
-    y[3] = v[3] + hi16<BF>(r[1]);
-  } else {
+    if (a.bf16)
+      v += f32x4{lo16<true>(r[0]), hi16<true>(r[0]), lo16<true>(r[1]), hi16<true>(r[1])};
+    else
+      v += f32x4{lo16<false>(r[0]), hi16<false>(r[0]), lo16<false>(r[1]), hi16<false>(r[1])};
+  } else if (a.epi == EPI_SWIGLU) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = EPI == EPI_SWIGLU ? silu(v[i]) * up[i] : v[i];
+    for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * up[i];
   }
-  *reinterpret_cast<u32x2*>(a.out + off) = u32x2{pack16<BF>(y[0], y[1]), pack16<BF>(y[2], y[3])};
+  const u32x2 h = a.bf16 ? u32x2{pack16<true>(v[0], v[1]), pack16<true>(v[2], v[3])}
+                         : u32x2{pack16<false>(v[0], v[1]), pack16<false>(v[2], v[3])};
+  *reinterpret_cast<u32x2*>(a.out + off) = h;
 }
 
 }  // namespace w4mx

@@ -73,11 +73,12 @@ int run_linear_mx(int op, const uint16_t* x, const void* w, const uint8_t* scale
   uint8_t* codes = static_cast<uint8_t*>(ws);
   uint8_t* xs = codes + w4::mx_scale_offset(T, K, fmt);
   const bool bf16 = dtype == W4_BF16;
-  if (x && w4::launch_mx_quant(x, K, T, K, bf16, fmt, codes, xs, hs) != hipSuccess) return W4_ERR_LAUNCH;
+  const bool fused = x && w4::mx_stream_fits(T, K, fmt);
+  if (x && !fused && w4::launch_mx_quant(x, K, T, K, bf16, fmt, codes, xs, hs) != hipSuccess) return W4_ERR_LAUNCH;
   w4::MxArgs a;
   a.xq = codes;
   a.xs = xs;
-  a.x = nullptr;
+  a.x = fused ? x : nullptr;
   a.w = static_cast<const uint8_t*>(w);
   a.ws = scales;
   a.res = res;
@@ -87,8 +88,9 @@ int run_linear_mx(int op, const uint16_t* x, const void* w, const uint8_t* scale
   a.K = K;
   a.KB = w4layout::num_kblocks(K);
   a.ldo = N;
-  const int epi = op == W4_OP_SWIGLU ? w4dev::EPI_SWIGLU : op == W4_OP_ADD ? w4dev::EPI_ADD : w4dev::EPI_STORE;
-  return launched(w4::launch_mx_stream(epi, bf16, fmt, a, hs));
+  a.epi = op == W4_OP_SWIGLU ? w4dev::EPI_SWIGLU : op == W4_OP_ADD ? w4dev::EPI_ADD : w4dev::EPI_STORE;
+  a.bf16 = bf16;
+  return launched(T <= 64 ? w4::launch_mx_stream(fmt, a, hs) : w4::launch_mx_wide(fmt, a, hs));
 }
 
 // kind: one of w4::NORM_*.  need: bytes of the workspace (0: the 16-bit output `out` instead).

@@ -24,10 +24,10 @@ void pack_tile(const uint8_t* codes, const uint8_t* scales, int K, int src, size
       const int b = kb * 4 + lane / 16;
       if (b < blocks) {
         std::memcpy(w + lane * 16, codes + n * (K / 2) + (size_t)b * 16, 16);
-        s[lane] = scales[n * blocks + b];
+        s[lane % 16 * 4 + lane / 16] = scales[n * blocks + b];
       } else {
         std::memset(w + lane * 16, 0, 16);
-        s[lane] = 0;
+        s[lane % 16 * 4 + lane / 16] = 0;
       }
     }
   }

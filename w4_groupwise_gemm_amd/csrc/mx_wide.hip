@@ -1,0 +1,174 @@
+// MX product at prefill widths: LDS-tiled, eight waves, two to a SIMD.
+#include "mx.h"
+#include "tile32.h"
+
+namespace w4 {
+namespace {
+
+using namespace w4mx;
+using t32::kXCD;
+using t32::rsrc;
+
+constexpr size_t kLds = 160 * 1024;
+constexpr int kGroupM = 8;
+
+// One stage: 128 columns of BM weight rows and BN tokens, with their scale bytes.
+template <int FMT, int BM, int BN, int kWaves, int WG_PER_CU>
+struct Stage {
+  static constexpr int kW = BM * 64, kX = BN * 16 * FMT;
+  static constexpr int kBytes = kW + kX + (BM + BN) * 4;
+  static constexpr int kFit = kLds / WG_PER_CU / kBytes;
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
+  static constexpr int kCN = (kW + kX) / 1024, kCL = (kCN + kWaves - 1) / kWaves;  // 1 KB loads of codes, per wave
+  static constexpr int kSN = (BM + BN) / 64, kSL = (kSN + kWaves - 1) / kWaves;    // loads of 256 scale bytes
+  static constexpr int kLoads = kCL + kSL;
+  static_assert(BM % 64 == 0 && BN % 64 == 0 && kStages >= 2, "whole loads, a ring");
+};
+
+__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voff, soff, 0, 0);
+}
+
+// WT: waves along the tokens (kWaves / WT along the rows).
+template <int FMT, int BM, int BN, int kWaves, int WT, int WG_PER_CU>
+__global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_kernel(MxArgs a, int nrb, int ntb) {
+  using S = Stage<FMT, BM, BN, kWaves, WG_PER_CU>;
+  constexpr int WR = kWaves / WT;
+  constexpr int MT = BM / 32 / WR, NT = BN / 32 / WT;  // 32-wide tiles per wave, rows and tokens
+  static_assert(MT * 32 * WR == BM && NT * 32 * WT == BN, "even tiles");
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, r = lane & 31;
+  const int wr = wave % WR, wt = wave / WR;
+  const int ntiles = a.rows / 16;
+  const int G = nrb * ntb, b = blockIdx.x, xcd = b % kXCD, l = b / kXCD;
+  const int idx = xcd * (G / kXCD) + min(xcd, G % kXCD) + l;
+  // Groups of kGroupM row blocks by every token block, rows first: the 32 workgroups that run
+  // together on one XCD cover about kGroupM x 4 tiles, so its L2 fetches each operand once.
+  const int grp = idx / (kGroupM * ntb), in = idx - grp * kGroupM * ntb;
+  const int gm = min(kGroupM, nrb - grp * kGroupM);
+  const int rb = grp * kGroupM + in % gm, tb = in / gm;
+  const int rt0 = rb * (BM / 16), tok0 = tb * BN;
+
+  // The wave's loads of a stage.  Lane offsets are those of k-block 0 (k-block kb adds a scalar); the
+  // last block's columns past K read past the resource's end, as zeros.
+  const int xstride = (int)mx_code_stride(a.K, FMT), sstride = (int)mx_scale_stride(a.K);
+  const int wtile = a.KB * 1024;  // bytes of a row tile's codes
+  int voff[S::kCL], vlast[S::kCL], step[S::kCL], soff[S::kSL], sstep[S::kSL];
+  __amdgpu_buffer_rsrc_t cr[S::kCL], sr[S::kSL];
+#pragma unroll
+  for (int i = 0; i < S::kCL; ++i) {
+    const int id = min(wave + kWaves * i, S::kCN - 1);
+    const bool isw = id < BM / 16;
+    cr[i] = rsrc(isw ? a.w : a.xq, isw ? (uint32_t)((size_t)ntiles * wtile) : (uint32_t)((size_t)a.T * xstride));
+    step[i] = isw ? 1024 : 16 * FMT;
+    // activations: rows of FMT chunks of 16 bytes, the chunk XORed with the row so that 8
+    // neighbouring rows' same chunk covers all banks
+    const int row = (id - BM / 16) * (64 / FMT) + lane / FMT;
+    const int chunk = (lane % FMT) ^ (FMT == 4 ? (row >> 1) & 3 : row & 7);
+    voff[i] = isw ? (rt0 + id) * wtile + lane * 16 : (tok0 + row) * xstride + chunk * 16;
+    vlast[i] = isw || (a.KB - 1) * 128 + chunk * (128 / FMT) < a.K ? voff[i] : (int)0x80000000u;
+  }
+#pragma unroll
+  for (int i = 0; i < S::kSL; ++i) {
+    const int id = min(wave + kWaves * i, S::kSN - 1);
+    const bool isw = id < BM / 64;
+    sr[i] = rsrc(isw ? a.ws : a.xs, isw ? (uint32_t)((size_t)ntiles * a.KB * 64) : (uint32_t)((size_t)a.T * sstride));
+    sstep[i] = isw ? 64 : 4;
+    soff[i] = isw ? (rt0 + id * 4 + (lane >> 4)) * a.KB * 64 + (lane & 15) * 4 : (tok0 + (id - BM / 64) * 64 + lane) * sstride;
+  }
+  auto load = [&](int kb, char* st) {
+    const bool last = kb == a.KB - 1;
+#pragma unroll
+    for (int i = 0; i < S::kCL; ++i)
+      to_lds16(cr[i], st + min(wave + kWaves * i, S::kCN - 1) * 1024, last ? vlast[i] : voff[i], kb * step[i]);
+#pragma unroll
+    for (int i = 0; i < S::kSL; ++i)
+      to_lds4(sr[i], st + S::kW + S::kX + min(wave + kWaves * i, S::kSN - 1) * 256, soff[i], kb * sstep[i]);
+  };
+
+  f32x16 acc[MT][NT] = {};
+#pragma unroll
+  for (int s = 0; s < S::kStages - 1; ++s) load(min(s, a.KB - 1), smem + s * S::kBytes);
+  int slot = 0, fill = S::kStages - 1;
+  for (int kb = 0; kb < a.KB; ++kb) {
+    wait_vmcnt<(S::kStages - 2) * S::kLoads>();
+    arrive_wait();
+    load(min(kb + S::kStages - 1, a.KB - 1), smem + fill * S::kBytes);
+    fill = fill == S::kStages - 1 ? 0 : fill + 1;
+    const char* st = smem + slot * S::kBytes;
+    slot = slot == S::kStages - 1 ? 0 : slot + 1;
+    const char* sc = st + S::kW + S::kX;
+    u32x4 w[MT][2];
+    uint32_t sw[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int rt = 2 * (wr * MT + i) + (r >> 4);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        w[i][u] = *reinterpret_cast<const u32x4*>(st + rt * 1024 + ((2 * u + h) * 16 + (r & 15)) * 16);
+      sw[i] = *reinterpret_cast<const uint32_t*>(sc + rt * 64 + (r & 15) * 4) >> (8 * h);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int row = (wt * NT + j) * 32 + r;
+      const char* xr = st + S::kW + row * 16 * FMT;
+      const uint32_t sx = *reinterpret_cast<const uint32_t*>(sc + BM * 4 + row * 4) >> (8 * h);
+      uint32_t x[2][FMT];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < FMT / 4; ++e) {
+          // E2M1: block 2 u + h.  E4M3: columns 64 u + 32 e + 16 h
+          const int chunk = (FMT == 4 ? 2 * u + h : 4 * u + 2 * e + h) ^ (FMT == 4 ? (row >> 1) & 3 : row & 7);
+          const u32x4 v = *reinterpret_cast<const u32x4*>(xr + chunk * 16);
+          x[u][4 * e] = v[0]; x[u][4 * e + 1] = v[1]; x[u][4 * e + 2] = v[2]; x[u][4 * e + 3] = v[3];
+        }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i][j] = mfma_mx32<FMT, 0>(w[i][0], sw[i], x[0], sx, acc[i][j]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i][j] = mfma_mx32<FMT, 1>(w[i][1], sw[i], x[1], sx, acc[i][j]);
+    }
+  }
+  wait_vmcnt<0>();  // no load may still write LDS after the workgroup has ended
+
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int t = tok0 + (wt * NT + j) * 32 + r;
+    if (t >= a.T) continue;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int rt = rt0 + 2 * (wr * MT + i);  // the tile's first row tile
+      auto quad = [&](int q) { return f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]}; };
+      if (a.epi == EPI_SWIGLU) {
+        if (rt < ntiles) {
+          store_quad_mx(a, t, 8 * rt + 4 * h, quad(0), quad(2));
+          store_quad_mx(a, t, 8 * rt + 8 + 4 * h, quad(1), quad(3));
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (rt + q / 2 < ntiles) store_quad_mx(a, t, 16 * rt + 8 * q + 4 * h, quad(q), quad(q));
+      }
+    }
+  }
+}
+
+template <int FMT, int BM, int BN, int kWaves, int WT, int WG_PER_CU>
+hipError_t run_tile(const MxArgs& a, hipStream_t stream) {
+  using S = Stage<FMT, BM, BN, kWaves, WG_PER_CU>;
+  const int nrb = (a.rows + BM - 1) / BM, ntb = (a.T + BN - 1) / BN;
+  return launch_kernel(&mx_wide_kernel<FMT, BM, BN, kWaves, WT, WG_PER_CU>, dim3(nrb * ntb), dim3(64 * kWaves),
+                       (size_t)S::kStages * S::kBytes, stream, a, nrb, ntb);
+}
+
+}  // namespace
+
+hipError_t launch_mx_wide(int fmt, const MxArgs& a, hipStream_t stream) {
+  return fmt == 4 ? run_tile<4, 256, 256, 8, 4, 1>(a, stream) : run_tile<8, 256, 256, 8, 4, 1>(a, stream);
+}
+
+}  // namespace w4
