@@ -15,6 +15,18 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int voff, int 
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
 }
 
+__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
+}
+// `bytes` (a multiple of 16) from the start of a resource into LDS, 1 KB a load, spread over the waves.
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t r, int from, char* lds, int bytes, int wave,
+                                            int waves, int lane) {
+  for (int i = wave * 1024; i < bytes; i += waves * 1024)
+    to_lds16(r, lds + i, i + lane * 16 < bytes ? from + lane * 16 : kOut, i);
+}
+// LDS taken by such a copy: whole loads.
+constexpr size_t lds_copy(size_t bytes) { return (bytes + 1023) / 1024 * 1024; }
+
 // The 16 packed pairs of block b (32 columns) of token t.
 __device__ __forceinline__ void load_block(__amdgpu_buffer_rsrc_t r, int off, uint32_t (&p)[16]) {
 #pragma unroll
@@ -53,91 +65,104 @@ __device__ __forceinline__ void finish(const MxArgs& a, f32x4 (*red)[RT][TT][64]
   }
 }
 
-// Weights of RT row tiles and one k-block.
+// Weight codes of RT row tiles and one k-block.
 template <int RT>
 struct WLoad {
   u32x4 c[RT];
-  uint32_t s[RT];
 };
 template <int RT>
 struct WSource {
   __amdgpu_buffer_rsrc_t w, s;
-  int KB, woff, soff;
+  int KB, off, scales;
   __device__ __forceinline__ WSource(const MxArgs& a, int rt0, int lane) : KB(a.KB) {
     const int ntiles = a.rows / 16;
     w = rsrc(a.w, (uint32_t)((size_t)ntiles * a.KB * 1024));
     s = rsrc(a.ws, (uint32_t)((size_t)ntiles * a.KB * 64));
-    woff = rt0 * a.KB * 1024 + lane * 16;
-    soff = rt0 * a.KB * 64 + (lane & 15) * 4 + (lane >> 4);
+    off = rt0 * a.KB * 1024 + lane * 16;
+    scales = rt0 * a.KB * 64;
   }
   // (row tiles past the last, and k-blocks at or past KB, are zeros)
   __device__ __forceinline__ void load(int kb, WLoad<RT>& o) const {
-    const bool on = kb < KB;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      o.c[i] = load16(w, on ? woff + i * KB * 1024 : kOut, kb * 1024);
-      o.s[i] = __builtin_amdgcn_raw_buffer_load_b8(s, on ? soff + i * KB * 64 : kOut, kb * 64, 0);
-    }
+    for (int i = 0; i < RT; ++i) o.c[i] = load16(w, kb < KB ? off + i * KB * 1024 : kOut, kb * 1024);
   }
 };
 
 // Bytes of LDS per token and k-block: codes, and one scale byte per block.
 constexpr int x_lds(int fmt) { return 16 * fmt + 4; }
 
-// Up to TP <= 16 tokens, held in LDS for all of K.  RT row tiles per workgroup of NW waves; wave w
-// takes k-blocks w, w + NW, .., DW of them in flight.  FUSED: the activations come in 16 bits and are
-// quantised on their way into LDS.
+// Up to TP <= 16 tokens, held in LDS for all of K beside the weights' scale bytes.  RT row tiles per
+// workgroup of NW waves; wave w takes k-blocks w, w + NW, .., DW of them in flight.  FUSED: the
+// activations come in 16 bits and are quantised on their way into LDS.
 template <int FMT, int RT, bool FUSED, int NW, int DW, bool BF>
 __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxArgs a, int tp_log) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ f32x4 red[NW][RT][1][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int rt0 = blockIdx.x * RT, nblk = a.K / 32, tp = 1 << tp_log;
-  uint8_t* xsc = reinterpret_cast<uint8_t*>(smem) + (size_t)a.KB * tp * 16 * FMT;  // scales [KB][4][tp]
+  char* wsc = smem;  // [RT][KB][16 rows][4]
+  char* xc = wsc + lds_copy((size_t)RT * a.KB * 64);  // activations [KB][FMT chunks of 16 bytes][tp]
+  uint8_t* xsc = reinterpret_cast<uint8_t*>(xc) + ((size_t)a.KB * 16 * FMT << tp_log);  // scales [KB][4][tp]
 
-  // activations: [KB][FMT chunks of 16 bytes][tp]; tokens past T repeat none (their outputs are not
-  // stored), blocks past K are zeros
   const int xstride = FUSED ? a.K * 2 : (int)mx_code_stride(a.K, FMT), sstride = (int)mx_scale_stride(a.K);
   const auto rx = rsrc(FUSED ? (const void*)a.x : a.xq, (uint32_t)((size_t)a.T * xstride));
   const auto rxs = rsrc(a.xs, (uint32_t)((size_t)a.T * sstride));
   const WSource<RT> src(a, rt0, lane);
   WLoad<RT> w[DW];
-  const int items = a.KB * 4 << tp_log;  // blocks, tokens fastest
-  auto put = [&](int it, const uint32_t (&c)[FMT], uint32_t byte) {
-    const int t = it & (tp - 1), b = it >> tp_log;
-    u32x4* dst = reinterpret_cast<u32x4*>(smem) + (((b >> 2) * FMT) << tp_log);
-#pragma unroll
-    for (int i = 0; i < FMT / 4; ++i)
-      dst[(((b & 3) * (FMT / 4) + i) << tp_log) + t] = u32x4{c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
-    xsc[it] = (uint8_t)byte;
+  // A thread's share of the activations: blocks `it`, tokens fastest.  Tokens past T and blocks past K
+  // are zeros.
+  const int items = a.KB * 4 << tp_log;
+  struct Item {
+    uint32_t v[FUSED ? 16 : FMT], byte;
   };
-  // the first block's loads ahead of the weights', the rest after them
-  uint32_t p[16], c[FMT], byte;
-  auto fetch = [&](int it) {
+  auto fetch = [&](int it, Item& o) {
     const int t = it & (tp - 1), b = it >> tp_log;
     const bool on = it < items && t < a.T && b < nblk;
     if constexpr (FUSED) {
-      load_block(rx, on ? t * xstride + b * 64 : kOut, p);
+      load_block(rx, on ? t * xstride + b * 64 : kOut, o.v);
     } else {
 #pragma unroll
       for (int i = 0; i < FMT / 4; ++i) {
         const u32x4 v = load16(rx, on ? t * xstride + b * 4 * FMT + 16 * i : kOut, 0);
-        c[4 * i] = v[0]; c[4 * i + 1] = v[1]; c[4 * i + 2] = v[2]; c[4 * i + 3] = v[3];
+        o.v[4 * i] = v[0]; o.v[4 * i + 1] = v[1]; o.v[4 * i + 2] = v[2]; o.v[4 * i + 3] = v[3];
       }
-      byte = __builtin_amdgcn_raw_buffer_load_b8(rxs, on ? t * sstride + b : kOut, 0, 0);
+      o.byte = __builtin_amdgcn_raw_buffer_load_b8(rxs, on ? t * sstride + b : kOut, 0, 0);
     }
   };
-  fetch(threadIdx.x);
+  auto put = [&](int it, Item& o) {
+    if (it >= items) return;
+    uint32_t c[FMT];
+    if constexpr (FUSED) {
+      o.byte = quantize_block<FMT, BF>(o.v, c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < FMT; ++i) c[i] = o.v[i];
+    }
+    const int t = it & (tp - 1), b = it >> tp_log;
+    u32x4* dst = reinterpret_cast<u32x4*>(xc) + (((b >> 2) * FMT + (b & 3) * (FMT / 4)) << tp_log) + t;
+#pragma unroll
+    for (int i = 0; i < FMT / 4; ++i) dst[i << tp_log] = u32x4{c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
+    xsc[it] = (uint8_t)o.byte;
+  };
+  // the first activations' loads ahead of the weights', so that the (in-order) wait for them leaves the
+  // weights in flight
+  constexpr int kFirst = 2, kStep = 64 * NW;
+  Item first[kFirst];
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) fetch(threadIdx.x + i * kStep, first[i]);
+  copy_to_lds(src.s, src.scales, wsc, RT * a.KB * 64, wave, NW, lane);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int d = 0; d < DW; ++d) src.load(wave + NW * d, w[d]);
   __builtin_amdgcn_sched_barrier(0);
-  for (int it = threadIdx.x; it < items; it += 64 * NW) {
-    if (it != (int)threadIdx.x) fetch(it);
-    if constexpr (FUSED) byte = quantize_block<FMT, BF>(p, c);
-    put(it, c, byte);
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) put(threadIdx.x + i * kStep, first[i]);
+  for (int it = threadIdx.x + kFirst * kStep; it < items; it += kStep) {
+    Item o;
+    fetch(it, o);
+    put(it, o);
   }
+  wait_vmcnt<DW * RT>();  // the scale bytes
   arrive_wait();
 
   f32x4 acc[RT][1] = {};
@@ -146,7 +171,7 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxArgs a, int tp_log
 #pragma unroll
     for (int d = 0; d < DW; ++d) {
       const int k = kb + NW * d, kx = min(k, a.KB - 1);  // (past the end the weights are zeros)
-      const u32x4* xp = reinterpret_cast<const u32x4*>(smem) + ((kx * FMT) << tp_log) + rr;
+      const u32x4* xp = reinterpret_cast<const u32x4*>(xc) + ((kx * FMT) << tp_log) + rr;
       uint32_t x[FMT];
 #pragma unroll
       for (int e = 0; e < FMT / 4; ++e) {
@@ -155,19 +180,40 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxArgs a, int tp_log
       }
       const uint32_t sx = xsc[((kx * 4 + g) << tp_log) + rr];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i][0] = mfma_mx16<FMT>(w[d].c[i], w[d].s[i], x, sx, acc[i][0]);
+      for (int i = 0; i < RT; ++i) {
+        const uint32_t sw = *reinterpret_cast<const uint8_t*>(wsc + (i * a.KB + kx) * 64 + r * 4 + g);
+        acc[i][0] = mfma_mx16<FMT>(w[d].c[i], sw, x, sx, acc[i][0]);
+      }
       src.load(k + NW * DW, w[d]);
     }
   }
-  finish<RT, 1, NW>(a, red, acc, rt0, 0, wave, lane);
+  __syncthreads();  // the sums take the memory of the activations and scales
+  finish<RT, 1, NW>(a, reinterpret_cast<f32x4(*)[RT][1][64]>(smem), acc, rt0, 0, wave, lane);
 }
 
-// Any number of tokens, TT tiles of 16 per workgroup, quantised activations straight from memory (L2) to
-// registers beside the weights, D k-blocks of both in flight: one in-order load counter serves
-// both, so neither may run ahead of the other.
+// TT token tiles of 16 per workgroup, quantised activations through a ring in LDS that each wave fills
+// and reads by itself (no barriers).  A unit is 128 bytes of every token's codes: one k-block of E4M3,
+// two of E2M1; wave w takes units w, w + NW, .., D of them (activations and weights) in flight.  The
+// scale bytes of all of K are in LDS from the start: read beside the codes they would touch
+// one cache line per token and unit, most of them still on their way for another wave.
 template <int FMT, int RT, int TT, int NW, int D>
-__global__ __launch_bounds__(64 * NW) void mx_direct_kernel(MxArgs a, int groups) {
-  __shared__ f32x4 red[NW][RT][TT][64];
+struct Ring {
+  static constexpr int KS = 8 / FMT;          // k-blocks per unit
+  static constexpr int kX = TT * 16 * 128;    // bytes of a unit's activations
+  static constexpr int kLoads = kX / 1024 + RT * KS;
+  static constexpr size_t kRing = (size_t)NW * D * kX, kRed = (size_t)NW * RT * TT * 1024;
+  static_assert(D * kLoads < 64, "load counter");
+  static size_t bytes(int K) {
+    const size_t b = kRing + lds_copy(TT * 16 * mx_scale_stride(K)) + lds_copy((size_t)RT * w4layout::num_kblocks(K) * 64);
+    return b > kRed ? b : kRed;
+  }
+};
+
+template <int FMT, int RT, int TT, int NW, int D>
+__global__ __launch_bounds__(64 * NW) void mx_ring_kernel(MxArgs a, int groups) {
+  using R = Ring<FMT, RT, TT, NW, D>;
+  constexpr int KS = R::KS, NX = R::kX / 1024;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int grp = blockIdx.x % groups, tok0 = blockIdx.x / groups * 16 * TT;
@@ -176,44 +222,70 @@ __global__ __launch_bounds__(64 * NW) void mx_direct_kernel(MxArgs a, int groups
   const int xstride = (int)mx_code_stride(a.K, FMT), sstride = (int)mx_scale_stride(a.K);
   const auto rx = rsrc(a.xq, (uint32_t)((size_t)a.T * xstride));
   const auto rxs = rsrc(a.xs, (uint32_t)((size_t)a.T * sstride));
-  struct X {
-    uint32_t c[TT][FMT], s[TT];
+  const int units = (a.KB + KS - 1) / KS;
+  char* ring = smem + wave * D * R::kX;
+  char* xsc = smem + R::kRing;                               // [16 TT tokens][sstride]
+  char* wsc = xsc + lds_copy((size_t)TT * 16 * sstride);     // [RT][KB][16 rows][4]
+  // a load covers 8 tokens x 128 bytes; the 16-byte chunk is XORed with the token so that 8
+  // neighbouring tokens' same chunk covers all banks
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const int xoff = (tok0 + (lane >> 3)) * xstride + chunk * 16;
+  const bool tail = (units - 1) * 128 + chunk * 16 >= xstride;  // past K in the last unit
+  struct WUnit {
+    WLoad<RT> k[KS];
   };
-  auto load_x = [&](int kb, X& o) {
+  auto load = [&](int u, char* slot, WUnit& w) {
+    const bool dead = u >= units || (u == units - 1 && tail);
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      const int t = tok0 + 16 * j + r;
+    for (int i = 0; i < NX; ++i) to_lds16(rx, slot + i * 1024, dead ? kOut : xoff + i * 8 * xstride, u * 128);
 #pragma unroll
-      for (int e = 0; e < FMT / 4; ++e) {
-        // E2M1: block g; E4M3: columns 64 e + 16 g .. + 15
-        const bool on = FMT == 4 ? kb * 128 + g * 32 < a.K : kb * 128 + 64 * e + 16 * g < a.K;
-        const u32x4 v = load16(rx, on ? t * xstride + 64 * e + 16 * g : kOut, kb * 16 * FMT);
-        o.c[j][4 * e] = v[0]; o.c[j][4 * e + 1] = v[1]; o.c[j][4 * e + 2] = v[2]; o.c[j][4 * e + 3] = v[3];
-      }
-      o.s[j] = __builtin_amdgcn_raw_buffer_load_b8(rxs, kb < a.KB ? t * sstride + g : kOut, kb * 4, 0);
-    }
+    for (int k = 0; k < KS; ++k) src.load(u * KS + k, w.k[k]);
   };
+  copy_to_lds(rxs, tok0 * sstride, xsc, TT * 16 * sstride, wave, NW, lane);
+  copy_to_lds(src.s, src.scales, wsc, RT * a.KB * 64, wave, NW, lane);
   f32x4 acc[RT][TT] = {};
-  WLoad<RT> w[D];
-  X x[D];
+  WUnit w[D];
 #pragma unroll
-  for (int d = 0; d < D; ++d) {
-    load_x(wave + NW * d, x[d]);
-    src.load(wave + NW * d, w[d]);
-  }
-  for (int kb = wave; kb < a.KB; kb += NW * D) {
+  for (int d = 0; d < D; ++d) load(wave + NW * d, ring + d * R::kX, w[d]);
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vmcnt<D * R::kLoads>();  // the scale bytes
+  arrive_wait();
+  for (int u = wave; u < units; u += NW * D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const int k = kb + NW * (d + D);
+      wait_vmcnt<(D - 1) * R::kLoads>();
+      __builtin_amdgcn_sched_barrier(0);
+      char* slot = ring + d * R::kX;
 #pragma unroll
-      for (int j = 0; j < TT; ++j)
+      for (int k = 0; k < KS; ++k) {
+        const int kb = min((u + NW * d) * KS + k, a.KB - 1);  // (past the end the weights are zeros)
+        uint32_t sw[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[i][j] = mfma_mx16<FMT>(w[d].c[i], w[d].s[i], x[d].c[j], x[d].s[j], acc[i][j]);
-      load_x(k, x[d]);
-      src.load(k, w[d]);
+        for (int i = 0; i < RT; ++i) sw[i] = *reinterpret_cast<const uint8_t*>(wsc + (i * a.KB + kb) * 64 + r * 4 + g);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          const char* row = slot + (16 * j + r) * 128;
+          uint32_t x[FMT];
+#pragma unroll
+          for (int e = 0; e < FMT / 4; ++e) {
+            // E2M1: block g of k-block k; E4M3: columns 64 e + 16 g .. + 15
+            const u32x4 v = *reinterpret_cast<const u32x4*>(row + (((4 * (FMT == 4 ? k : e) + g) ^ (r & 7)) << 4));
+            x[4 * e] = v[0]; x[4 * e + 1] = v[1]; x[4 * e + 2] = v[2]; x[4 * e + 3] = v[3];
+          }
+          const uint32_t sx = *reinterpret_cast<const uint8_t*>(xsc + (16 * j + r) * sstride + kb * 4 + g);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) acc[i][j] = mfma_mx16<FMT>(w[d].k[k].c[i], sw[i], x, sx, acc[i][j]);
+        }
+      }
+      // every read of the slot has returned before it is filled again
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      __builtin_amdgcn_sched_barrier(0);
+      load(u + NW * (d + D), slot, w[d]);
     }
   }
-  finish<RT, TT, NW>(a, red, acc, rt0, tok0, wave, lane);
+  wait_vmcnt<0>();
+  __syncthreads();  // the sums take the ring's memory
+  finish<RT, TT, NW>(a, reinterpret_cast<f32x4(*)[RT][TT][64]>(smem), acc, rt0, tok0, wave, lane);
 }
 
 template <int FMT, int RT, int NW, int DW>
@@ -221,25 +293,26 @@ hipError_t run_stream(const MxArgs& a, hipStream_t stream) {
   const dim3 grid((a.rows / 16 + RT - 1) / RT);
   int tp_log = 0;
   while ((1 << tp_log) < a.T) ++tp_log;
-  const size_t lds = (size_t)(a.KB << tp_log) * x_lds(FMT);
+  const size_t need = lds_copy((size_t)RT * a.KB * 64) + (size_t)(a.KB << tp_log) * x_lds(FMT), red = (size_t)NW * RT * 1024;
+  const size_t lds = need > red ? need : red;
   auto k = !a.x ? &mx_stream_kernel<FMT, RT, false, NW, DW, false>
                 : a.bf16 ? &mx_stream_kernel<FMT, RT, true, NW, DW, true> : &mx_stream_kernel<FMT, RT, true, NW, DW, false>;
   return launch_kernel(k, grid, dim3(64 * NW), lds, stream, a, tp_log);
 }
 
 template <int FMT, int RT, int TT, int NW, int D>
-hipError_t run_direct(const MxArgs& a, hipStream_t stream) {
+hipError_t run_ring(const MxArgs& a, hipStream_t stream) {
   const int groups = (a.rows / 16 + RT - 1) / RT;
-  return launch_kernel(&mx_direct_kernel<FMT, RT, TT, NW, D>, dim3(groups * ((a.T + 16 * TT - 1) / (16 * TT))),
-                       dim3(64 * NW), 0, stream, a, groups);
+  return launch_kernel(&mx_ring_kernel<FMT, RT, TT, NW, D>, dim3(groups * ((a.T + 16 * TT - 1) / (16 * TT))),
+                       dim3(64 * NW), Ring<FMT, RT, TT, NW, D>::bytes(a.K), stream, a, groups);
 }
 
 template <int FMT>
 hipError_t pick(const MxArgs& a, hipStream_t stream) {
   if (mx_stream_fits(a.T, a.K, FMT)) return run_stream<FMT, 2, 8, 4>(a, stream);
-  if (a.T <= 16) return run_direct<FMT, 2, 1, 8, 4>(a, stream);
-  if (a.T <= 32) return run_direct<FMT, 2, 2, 8, 3>(a, stream);
-  return run_direct<FMT, 2, 4, 8, 2>(a, stream);
+  if (a.T <= 16) return run_ring<FMT, 2, 1, 8, 3>(a, stream);
+  if (a.T <= 32) return run_ring<FMT, 2, 2, 8, 3>(a, stream);
+  return run_ring<FMT, 2, 4, 4, 2>(a, stream);
 }
 
 }  // namespace
