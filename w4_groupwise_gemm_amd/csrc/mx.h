@@ -55,10 +55,21 @@ hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int T,
 hipError_t launch_a8_dequant(const int8_t* codes, const float* scales, int T, int K, bool bf16, uint16_t* out,
                              hipStream_t stream);
 hipError_t launch_norm(int kind, bool bf16, const NormArgs& a, hipStream_t stream);
-// Whether the streaming kernel holds T x K activations in LDS; it then also quantises them itself.
-bool mx_stream_fits(int T, int K, int fmt);
-hipError_t launch_mx_stream(int fmt, const MxArgs& a, hipStream_t stream);
-hipError_t launch_mx_wide(int fmt, const MxArgs& a, hipStream_t stream);
+// The product's kernels.  Streaming (mx_stream.hip): rt row tiles per workgroup, T <= 16 tokens in LDS,
+// which it quantises itself where a.x is given.  Ring (mx_stream.hip): rt row tiles by tt (1, 2 or 4)
+// token tiles of 16.  Wide (mx_wide.hip): one of kMxWide; the last (kMxWide320) for MXFP4 activations only.
+// A SwiGLU pair needs an even rt.  mx_*_lds: bytes of LDS a workgroup takes (at most kMxLds).
+constexpr size_t kMxLds = 160 * 1024;
+size_t mx_stream_lds(int T, int K, int fmt, int rt);
+size_t mx_ring_lds(int K, int rt, int tt);
+struct MxTile {
+  int rows, tokens;
+};
+constexpr MxTile kMxWide[] = {{64, 64}, {128, 64}, {128, 128}, {256, 128}, {320, 256}};
+constexpr int kMxWide320 = 4;
+hipError_t launch_mx_stream(int fmt, int rt, const MxArgs& a, hipStream_t stream);
+hipError_t launch_mx_ring(int fmt, int rt, int tt, const MxArgs& a, hipStream_t stream);
+hipError_t launch_mx_wide(int fmt, int tile, const MxArgs& a, hipStream_t stream);
 
 // Status of the current device (W4_OK when it is a gfx950); defined in api.hip.
 int device_status();

@@ -48,6 +48,62 @@ int check_ws(const void* ws, size_t bytes, size_t need, std::initializer_list<Ra
 
 int launched(hipError_t e) { return e == hipSuccess ? W4_OK : W4_ERR_LAUNCH; }
 
+// ---- routes of the product
+enum RouteKind { STREAM, RING, WIDE };
+struct Route {
+  RouteKind kind;
+  int rt, tt;  // row tiles and token tiles per workgroup (wide: rt is the index in kMxWide)
+};
+
+// Microseconds per 128 columns of a launch whose fullest compute unit runs m workgroups: c0 + c1 * m,
+// fitted to launches of 128 to 2560 workgroups at K = 5120 (every kernel within 12 % of its fit).
+struct Cost {
+  double c0, c1;
+};
+double cost(Cost c, int64_t workgroups) { return c.c0 + c.c1 * (double)((workgroups + 255) / 256); }
+const Cost kWideCost[2][5] = {
+    {{0.125, 0.16}, {0.12, 0.28}, {0.25, 0.37}, {0.45, 0.57}, {0, 1.62}},  // MXFP4 activations
+    {{0.135, 0.184}, {0.18, 0.295}, {0.2, 0.5}, {0.3, 0.86}, {0, 1e9}},    // MXFP8
+};
+
+// The cheapest kernel for the shape.  Few activations (up to 16 tokens): the streaming kernel, which
+// saves the launch for the quantisation (about 2.3 us) but quantises in every workgroup, m of them one
+// after another on a compute unit.  Measured at 12288 x 5120 (m = 1): 8 tokens 10.9 us against the ring's
+// 11.4, 16 tokens 13.7 against 11.9; at the 2 x 17408 x 5120 pair (m = 5): 4 tokens 23.0 against 24.6,
+// 8 tokens 27.8 against 25.0; at 5120 x 17408 (m = 1): 2 tokens 12.6 against 14.5, 4 tokens 15.7 against
+// 15.4.  Otherwise whichever of the ring (blocks of up to 64 tokens) and the wide tiles the fits above
+// name.
+constexpr double kStreamWork = 65536;  // T * K * (1 + m / 4)
+Route pick(int op, int T, int rows, int K, int fmt) {
+  const int n = rows / 16, step = op == W4_OP_SWIGLU ? 2 : 1;
+  Route best = {WIDE, 0, 0};
+  double least = 1e30;
+  if (T <= 16) {
+    for (int rt = step; rt <= 4; rt += step) {
+      if (w4::mx_stream_lds(T, K, fmt, rt) > w4::kMxLds) continue;
+      const double c = cost({0, 0.3 + rt}, (n + rt - 1) / rt);
+      if (c < least) least = c, best = {STREAM, rt, 0};
+    }
+    const double m = best.kind == STREAM ? ((n + best.rt - 1) / best.rt + 255) / 256 : 0;
+    if (best.kind == STREAM && (double)T * K * (1 + m / 4) <= kStreamWork) return best;
+    least = 1e30;
+  }
+  const int tt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  for (int rt = step; rt <= 4; rt += step) {
+    if (w4::mx_ring_lds(K, rt, tt) > w4::kMxLds) continue;
+    const Cost c = fmt == 4 ? Cost{0.12, 0.01 * tt + 0.047 * rt} : Cost{0.14, 0.0125 * tt + 0.056 * rt};
+    const double v = cost(c, (int64_t)((n + rt - 1) / rt) * ((T + 16 * tt - 1) / (16 * tt)));
+    if (v < least) least = v, best = {RING, rt, tt};
+  }
+  if (T <= 64 && best.kind == RING) return best;
+  for (int i = 0; i < 5; ++i) {
+    const w4::MxTile t = w4::kMxWide[i];
+    const double v = cost(kWideCost[fmt == 8][i], (int64_t)((rows + t.rows - 1) / t.rows) * ((T + t.tokens - 1) / t.tokens));
+    if (v < least) least = v, best = {WIDE, i, 0};
+  }
+  return best;
+}
+
 int run_linear_mx(int op, const uint16_t* x, const void* w, const uint8_t* scales, const uint16_t* res, int T, int N,
                   int K, int fmt, int dtype, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
   if (!fmt_ok(fmt) || !dtype_ok(dtype)) return W4_ERR_UNSUPPORTED;
@@ -73,7 +129,8 @@ int run_linear_mx(int op, const uint16_t* x, const void* w, const uint8_t* scale
   uint8_t* codes = static_cast<uint8_t*>(ws);
   uint8_t* xs = codes + w4::mx_scale_offset(T, K, fmt);
   const bool bf16 = dtype == W4_BF16;
-  const bool fused = x && w4::mx_stream_fits(T, K, fmt);
+  const Route route = pick(op, T, rows, K, fmt);
+  const bool fused = x && route.kind == STREAM;
   if (x && !fused && w4::launch_mx_quant(x, K, T, K, bf16, fmt, codes, xs, hs) != hipSuccess) return W4_ERR_LAUNCH;
   w4::MxArgs a;
   a.xq = codes;
@@ -90,7 +147,9 @@ int run_linear_mx(int op, const uint16_t* x, const void* w, const uint8_t* scale
   a.ldo = N;
   a.epi = op == W4_OP_SWIGLU ? w4dev::EPI_SWIGLU : op == W4_OP_ADD ? w4dev::EPI_ADD : w4dev::EPI_STORE;
   a.bf16 = bf16;
-  return launched(T <= 64 ? w4::launch_mx_stream(fmt, a, hs) : w4::launch_mx_wide(fmt, a, hs));
+  return launched(route.kind == STREAM ? w4::launch_mx_stream(fmt, route.rt, a, hs)
+                  : route.kind == RING ? w4::launch_mx_ring(fmt, route.rt, route.tt, a, hs)
+                                       : w4::launch_mx_wide(fmt, route.rt, a, hs));
 }
 
 // kind: one of w4::NORM_*.  need: bytes of the workspace (0: the 16-bit output `out` instead).

@@ -201,12 +201,8 @@ struct Ring {
   static constexpr int KS = 8 / FMT;          // k-blocks per unit
   static constexpr int kX = TT * 16 * 128;    // bytes of a unit's activations
   static constexpr int kLoads = kX / 1024 + RT * KS;
-  static constexpr size_t kRing = (size_t)NW * D * kX, kRed = (size_t)NW * RT * TT * 1024;
+  static constexpr size_t kRing = (size_t)NW * D * kX;
   static_assert(D * kLoads < 64, "load counter");
-  static size_t bytes(int K) {
-    const size_t b = kRing + lds_copy(TT * 16 * mx_scale_stride(K)) + lds_copy((size_t)RT * w4layout::num_kblocks(K) * 64);
-    return b > kRed ? b : kRed;
-  }
 };
 
 template <int FMT, int RT, int TT, int NW, int D>
@@ -288,43 +284,85 @@ __global__ __launch_bounds__(64 * NW) void mx_ring_kernel(MxArgs a, int groups) 
   finish<RT, TT, NW>(a, reinterpret_cast<f32x4(*)[RT][TT][64]>(smem), acc, rt0, tok0, wave, lane);
 }
 
-template <int FMT, int RT, int NW, int DW>
+constexpr int kStreamWaves = 8, kStreamDepth = 2;
+// Waves of the ring kernel by token tiles: eight while two slots each leave room for the scale bytes of
+// long rows, four at 64 tokens.
+constexpr int ring_waves(int tt) { return tt == 4 ? 4 : 8; }
+constexpr int kRingDepth = 2;
+
+template <int FMT, int RT>
 hipError_t run_stream(const MxArgs& a, hipStream_t stream) {
-  const dim3 grid((a.rows / 16 + RT - 1) / RT);
+  constexpr int NW = kStreamWaves, DW = kStreamDepth;
   int tp_log = 0;
   while ((1 << tp_log) < a.T) ++tp_log;
-  const size_t need = lds_copy((size_t)RT * a.KB * 64) + (size_t)(a.KB << tp_log) * x_lds(FMT), red = (size_t)NW * RT * 1024;
-  const size_t lds = need > red ? need : red;
   auto k = !a.x ? &mx_stream_kernel<FMT, RT, false, NW, DW, false>
                 : a.bf16 ? &mx_stream_kernel<FMT, RT, true, NW, DW, true> : &mx_stream_kernel<FMT, RT, true, NW, DW, false>;
-  return launch_kernel(k, grid, dim3(64 * NW), lds, stream, a, tp_log);
+  return launch_kernel(k, dim3((a.rows / 16 + RT - 1) / RT), dim3(64 * NW), mx_stream_lds(a.T, a.K, FMT, RT), stream, a,
+                       tp_log);
 }
 
-template <int FMT, int RT, int TT, int NW, int D>
+template <int FMT, int RT, int TT>
 hipError_t run_ring(const MxArgs& a, hipStream_t stream) {
-  const int groups = (a.rows / 16 + RT - 1) / RT;
-  return launch_kernel(&mx_ring_kernel<FMT, RT, TT, NW, D>, dim3(groups * ((a.T + 16 * TT - 1) / (16 * TT))),
-                       dim3(64 * NW), Ring<FMT, RT, TT, NW, D>::bytes(a.K), stream, a, groups);
+  const int groups = (a.rows / 16 + RT - 1) / RT, blocks = (a.T + 16 * TT - 1) / (16 * TT);
+  constexpr int NW = ring_waves(TT);
+  return launch_kernel(&mx_ring_kernel<FMT, RT, TT, NW, kRingDepth>, dim3(groups * blocks), dim3(64 * NW),
+                       mx_ring_lds(a.K, RT, TT), stream, a, groups);
+}
+
+template <int FMT, int RT>
+hipError_t ring_rt(int tt, const MxArgs& a, hipStream_t stream) {
+  switch (tt) {
+    case 1: return run_ring<FMT, RT, 1>(a, stream);
+    case 2: return run_ring<FMT, RT, 2>(a, stream);
+    case 4: return run_ring<FMT, RT, 4>(a, stream);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 template <int FMT>
-hipError_t pick(const MxArgs& a, hipStream_t stream) {
-  if (mx_stream_fits(a.T, a.K, FMT)) return run_stream<FMT, 2, 8, 4>(a, stream);
-  if (a.T <= 16) return run_ring<FMT, 2, 1, 8, 3>(a, stream);
-  if (a.T <= 32) return run_ring<FMT, 2, 2, 8, 3>(a, stream);
-  return run_ring<FMT, 2, 4, 4, 2>(a, stream);
+hipError_t stream_fmt(int rt, const MxArgs& a, hipStream_t stream) {
+  switch (rt) {
+    case 1: return run_stream<FMT, 1>(a, stream);
+    case 2: return run_stream<FMT, 2>(a, stream);
+    case 3: return run_stream<FMT, 3>(a, stream);
+    case 4: return run_stream<FMT, 4>(a, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+template <int FMT>
+hipError_t ring_fmt(int rt, int tt, const MxArgs& a, hipStream_t stream) {
+  switch (rt) {
+    case 1: return ring_rt<FMT, 1>(tt, a, stream);
+    case 2: return ring_rt<FMT, 2>(tt, a, stream);
+    case 3: return ring_rt<FMT, 3>(tt, a, stream);
+    case 4: return ring_rt<FMT, 4>(tt, a, stream);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
-bool mx_stream_fits(int T, int K, int fmt) {
-  int tp = 1;
-  while (tp < T) tp *= 2;
-  return T <= 16 && (size_t)w4layout::num_kblocks(K) * tp * x_lds(fmt) <= 96 * 1024;
+size_t mx_stream_lds(int T, int K, int fmt, int rt) {
+  size_t tp = 1;
+  while (tp < (size_t)T) tp *= 2;
+  const size_t kb = w4layout::num_kblocks(K);
+  const size_t need = lds_copy(rt * kb * 64) + kb * tp * x_lds(fmt), red = (size_t)kStreamWaves * rt * 1024;
+  return need > red ? need : red;
 }
 
-hipError_t launch_mx_stream(int fmt, const MxArgs& a, hipStream_t stream) {
-  return fmt == 4 ? pick<4>(a, stream) : pick<8>(a, stream);
+size_t mx_ring_lds(int K, int rt, int tt) {
+  const size_t ring = (size_t)ring_waves(tt) * kRingDepth * tt * 2048, red = (size_t)ring_waves(tt) * rt * tt * 1024;
+  const size_t b = ring + lds_copy(tt * 16 * mx_scale_stride(K)) + lds_copy((size_t)rt * w4layout::num_kblocks(K) * 64);
+  return b > red ? b : red;
+}
+
+hipError_t launch_mx_stream(int fmt, int rt, const MxArgs& a, hipStream_t stream) {
+  return fmt == 4 ? stream_fmt<4>(rt, a, stream) : stream_fmt<8>(rt, a, stream);
+}
+
+hipError_t launch_mx_ring(int fmt, int rt, int tt, const MxArgs& a, hipStream_t stream) {
+  return fmt == 4 ? ring_fmt<4>(rt, tt, a, stream) : ring_fmt<8>(rt, tt, a, stream);
 }
 
 }  // namespace w4

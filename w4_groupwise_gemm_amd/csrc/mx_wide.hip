@@ -1,4 +1,6 @@
 // MX product at prefill widths: LDS-tiled, eight waves, two to a SIMD.
+#include <type_traits>
+
 #include "mx.h"
 #include "tile32.h"
 
@@ -9,29 +11,33 @@ using namespace w4mx;
 using t32::kXCD;
 using t32::rsrc;
 
-constexpr size_t kLds = 160 * 1024;
 constexpr int kGroupM = 8;
 
-// One stage: 128 columns of BM weight rows and BN tokens, with their scale bytes.
+// A ring of stages, each 128 columns of BM weight rows and BN tokens, and two buffers of the scale
+// bytes of 512 columns (four stages): 16 bytes per row and token, loaded with the last stage before
+// they are needed.
 template <int FMT, int BM, int BN, int kWaves, int WG_PER_CU>
 struct Stage {
-  static constexpr int kW = BM * 64, kX = BN * 16 * FMT;
-  static constexpr int kBytes = kW + kX + (BM + BN) * 4;
-  static constexpr int kFit = kLds / WG_PER_CU / kBytes;
+  static constexpr int kW = BM * 64, kX = BN * 16 * FMT, kCodes = kW + kX;
+  static constexpr int kScales = (BM + BN) * 16;
+  static constexpr int kFit = ((int)kMxLds / WG_PER_CU - 2 * kScales) / kCodes;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
-  static constexpr int kCN = (kW + kX) / 1024, kCL = (kCN + kWaves - 1) / kWaves;  // 1 KB loads of codes, per wave
-  static constexpr int kSN = (BM + BN) / 64, kSL = (kSN + kWaves - 1) / kWaves;    // loads of 256 scale bytes
-  static constexpr int kLoads = kCL + kSL;
+  static constexpr int kBytes = kStages * kCodes + 2 * kScales;
+  static constexpr int kCN = kCodes / 1024, kCL = (kCN + kWaves - 1) / kWaves;     // 1 KB loads of codes, per wave
+  static constexpr int kSN = kScales / 1024, kSL = (kSN + kWaves - 1) / kWaves;    // of scales, every fourth stage
   static_assert(BM % 64 == 0 && BN % 64 == 0 && kStages >= 2, "whole loads, a ring");
+  // loads issued after those of a stage at position p of its four that may still be in flight when it
+  // is read
+  static constexpr int later(int p) {
+    int n = 0;
+    for (int s = p + 1; s <= p + kStages - 2; ++s) n += kCL + (s % 4 == 3 ? kSL : 0);
+    return n;
+  }
 };
 
 __device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
 }
-__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t r, char* lds, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voff, soff, 0, 0);
-}
-
 // WT: waves along the tokens (kWaves / WT along the rows).
 template <int FMT, int BM, int BN, int kWaves, int WT, int WG_PER_CU>
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_kernel(MxArgs a, int nrb, int ntb) {
@@ -74,34 +80,43 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_k
   }
 #pragma unroll
   for (int i = 0; i < S::kSL; ++i) {
+    // 512 columns: 256 bytes of a row tile (16 lanes), 16 bytes of a token (one lane)
     const int id = min(wave + kWaves * i, S::kSN - 1);
     const bool isw = id < BM / 64;
     sr[i] = rsrc(isw ? a.ws : a.xs, isw ? (uint32_t)((size_t)ntiles * a.KB * 64) : (uint32_t)((size_t)a.T * sstride));
-    sstep[i] = isw ? 64 : 4;
-    soff[i] = isw ? (rt0 + id * 4 + (lane >> 4)) * a.KB * 64 + (lane & 15) * 4 : (tok0 + (id - BM / 64) * 64 + lane) * sstride;
+    sstep[i] = isw ? 256 : 16;
+    soff[i] = isw ? (rt0 + id * 4 + (lane >> 4)) * a.KB * 64 + (lane & 15) * 16 : (tok0 + (id - BM / 64) * 64 + lane) * sstride;
   }
+  char* scales = smem + S::kStages * S::kCodes;
   auto load = [&](int kb, char* st) {
     const bool last = kb == a.KB - 1;
 #pragma unroll
     for (int i = 0; i < S::kCL; ++i)
       to_lds16(cr[i], st + min(wave + kWaves * i, S::kCN - 1) * 1024, last ? vlast[i] : voff[i], kb * step[i]);
+  };
+  // (past the last columns: bytes that nothing reads)
+  auto load_scales = [&](int q) {
 #pragma unroll
     for (int i = 0; i < S::kSL; ++i)
-      to_lds4(sr[i], st + S::kW + S::kX + min(wave + kWaves * i, S::kSN - 1) * 256, soff[i], kb * sstep[i]);
+      to_lds16(sr[i], scales + (q & 1) * S::kScales + min(wave + kWaves * i, S::kSN - 1) * 1024, soff[i], q * sstep[i]);
   };
 
   f32x16 acc[MT][NT] = {};
+  load_scales(0);
 #pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) load(min(s, a.KB - 1), smem + s * S::kBytes);
+  for (int s = 0; s < S::kStages - 1; ++s) load(min(s, a.KB - 1), smem + s * S::kCodes);
   int slot = 0, fill = S::kStages - 1;
-  for (int kb = 0; kb < a.KB; ++kb) {
-    wait_vmcnt<(S::kStages - 2) * S::kLoads>();
+  auto step4 = [&](int kb, auto pos) {
+    constexpr int P = decltype(pos)::value;  // kb % 4
+    wait_vmcnt<S::later(P)>();
     arrive_wait();
-    load(min(kb + S::kStages - 1, a.KB - 1), smem + fill * S::kBytes);
+    load(min(kb + S::kStages - 1, a.KB - 1), smem + fill * S::kCodes);
+    // (the buffer's previous bytes were last read at least one stage ago)
+    if constexpr ((P + S::kStages - 1) % 4 == 3) load_scales((kb + S::kStages) / 4);
     fill = fill == S::kStages - 1 ? 0 : fill + 1;
-    const char* st = smem + slot * S::kBytes;
+    const char* st = smem + slot * S::kCodes;
     slot = slot == S::kStages - 1 ? 0 : slot + 1;
-    const char* sc = st + S::kW + S::kX;
+    const char* sc = scales + (kb / 4 & 1) * S::kScales;
     u32x4 w[MT][2];
     uint32_t sw[MT];
 #pragma unroll
@@ -110,13 +125,13 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_k
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         w[i][u] = *reinterpret_cast<const u32x4*>(st + rt * 1024 + ((2 * u + h) * 16 + (r & 15)) * 16);
-      sw[i] = *reinterpret_cast<const uint32_t*>(sc + rt * 64 + (r & 15) * 4) >> (8 * h);
+      sw[i] = *reinterpret_cast<const uint32_t*>(sc + rt * 256 + P * 64 + (r & 15) * 4) >> (8 * h);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int row = (wt * NT + j) * 32 + r;
       const char* xr = st + S::kW + row * 16 * FMT;
-      const uint32_t sx = *reinterpret_cast<const uint32_t*>(sc + BM * 4 + row * 4) >> (8 * h);
+      const uint32_t sx = *reinterpret_cast<const uint32_t*>(sc + BM * 16 + row * 16 + P * 4) >> (8 * h);
       uint32_t x[2][FMT];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -132,6 +147,12 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_k
 #pragma unroll
       for (int i = 0; i < MT; ++i) acc[i][j] = mfma_mx32<FMT, 1>(w[i][1], sw[i], x[1], sx, acc[i][j]);
     }
+  };
+  for (int kb = 0; kb < a.KB; kb += 4) {
+    step4(kb, std::integral_constant<int, 0>{});
+    if (kb + 1 < a.KB) step4(kb + 1, std::integral_constant<int, 1>{});
+    if (kb + 2 < a.KB) step4(kb + 2, std::integral_constant<int, 2>{});
+    if (kb + 3 < a.KB) step4(kb + 3, std::integral_constant<int, 3>{});
   }
   wait_vmcnt<0>();  // no load may still write LDS after the workgroup has ended
 
@@ -157,18 +178,34 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_k
   }
 }
 
-template <int FMT, int BM, int BN, int kWaves, int WT, int WG_PER_CU>
+// The tiles of kMxWide: waves, waves along the tokens, workgroups per compute unit.
+template <int FMT, int TILE, int kWaves, int WT, int WG_PER_CU>
 hipError_t run_tile(const MxArgs& a, hipStream_t stream) {
+  constexpr int BM = kMxWide[TILE].rows, BN = kMxWide[TILE].tokens;
   using S = Stage<FMT, BM, BN, kWaves, WG_PER_CU>;
   const int nrb = (a.rows + BM - 1) / BM, ntb = (a.T + BN - 1) / BN;
   return launch_kernel(&mx_wide_kernel<FMT, BM, BN, kWaves, WT, WG_PER_CU>, dim3(nrb * ntb), dim3(64 * kWaves),
-                       (size_t)S::kStages * S::kBytes, stream, a, nrb, ntb);
+                       (size_t)S::kBytes, stream, a, nrb, ntb);
+}
+
+template <int FMT>
+hipError_t pick_tile(int tile, const MxArgs& a, hipStream_t stream) {
+  switch (tile) {
+    case 0: return run_tile<FMT, 0, 4, 2, 2>(a, stream);
+    case 1: return run_tile<FMT, 1, 4, 1, 1>(a, stream);
+    case 2: return run_tile<FMT, 2, 4, 2, 2>(a, stream);
+    case 3: return run_tile<FMT, 3, 4, 2, 2>(a, stream);
+    case kMxWide320:
+      if constexpr (FMT == 4) return run_tile<FMT, kMxWide320, 8, 4, 1>(a, stream);
+      [[fallthrough]];
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
-hipError_t launch_mx_wide(int fmt, const MxArgs& a, hipStream_t stream) {
-  return fmt == 4 ? run_tile<4, 256, 256, 8, 4, 1>(a, stream) : run_tile<8, 256, 256, 8, 4, 1>(a, stream);
+hipError_t launch_mx_wide(int fmt, int tile, const MxArgs& a, hipStream_t stream) {
+  return fmt == 4 ? pick_tile<4>(tile, a, stream) : pick_tile<8>(tile, a, stream);
 }
 
 }  // namespace w4
