@@ -293,7 +293,10 @@ int w4_dequantize_mx(const void* workspace, size_t workspace_bytes, int T, int K
  * holds this T x K activation, as w4_quantize_mx or w4_rmsnorm_mx wrote it.  Products of E4M3
  * elements are aligned inside the matrix unit to the largest of a few neighbours and lose what lies
  * about 2^-15 below it; products of E2M1 elements are summed exactly inside a step.
- * out == residual (exactly) is allowed. */
+ * out == residual (exactly) is allowed.  With x given the workspace must hold
+ * w4_linear_mx_workspace_bytes bytes, and may be NULL where that is 0 (few activations: one kernel
+ * quantises and multiplies; otherwise two kernels are enqueued).  A product does not promise to leave
+ * the quantised x in the workspace. */
 int w4_linear_mx(const uint16_t* x, const void* w, const uint8_t* scales, int T, int N, int K, int fmt,
                  int dtype, uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
 int w4_linear_swiglu_mx(const uint16_t* x, const void* w_pair, const uint8_t* scales_pair, int T, int N,
@@ -302,6 +305,13 @@ int w4_linear_swiglu_mx(const uint16_t* x, const void* w_pair, const uint8_t* sc
 int w4_linear_add_mx(const uint16_t* x, const void* w, const uint8_t* scales, const uint16_t* residual,
                      int T, int N, int K, int fmt, int dtype, uint16_t* out, void* workspace,
                      size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace a product on 16-bit activations needs: w4_mx_workspace_bytes(T, K, fmt), or 0 where
+ * it needs none (or the shape, op or fmt is invalid). */
+size_t w4_linear_mx_workspace_bytes(int op, int T, int N, int K, int fmt);
+
+/* Name of the kernel a product of this shape runs (static string); NULL for an invalid shape. */
+const char* w4_mx_route_name(int op, int T, int N, int K, int fmt);
 
 /* ---- root-mean-square norm, with the residual's addition in front of it:
  *   h = x + residual,   y = h / sqrt(mean(h^2) + eps) * weight     (per token row, in fp32)

@@ -117,6 +117,7 @@ def test_residual_in_place_workspace_and_guard_rows(T):
     c.r = buf[:T]
     need = w4.mx_workspace_bytes(T, 288, 8)
     ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN scales and codes
+    assert need >= w4.linear_mx_workspace_bytes(2, T, 64, 288, 8)
     assert c.run(out=buf[:T], workspace=ws).data_ptr() == buf.data_ptr()
     assert torch.equal(buf[:T], want) and (buf[T:] == 3).all()
     assert (ws[need:] == 0xFF).all()

@@ -150,16 +150,17 @@ def _lin(fn="w4_linear_mx", x=X, w=W, s=S, r=R, T=4, N=64, K=256, fmt=8, dtype=0
 def test_linear_mx_refusals(fn):
     assert _lin(fn, fmt=6) == -2 and _lin(fn, dtype=2) == -2
     for bad in (dict(T=-1), dict(N=0), dict(N=40), dict(K=0), dict(K=48), dict(w=None), dict(s=None), dict(out=None),
-                dict(ws=None), dict(nb=w4.mx_workspace_bytes(4, 256, 8) - 1), dict(N=1 << 25), dict(K=1 << 25)):
+                dict(ws=None, x=None), dict(nb=w4.mx_workspace_bytes(4, 256, 8) - 1, x=None), dict(N=1 << 25), dict(K=1 << 25),
+                dict(T=40, ws=None), dict(T=40, nb=w4.mx_workspace_bytes(40, 256, 8) - 1)):
         assert _lin(fn, **bad) == -1, bad
-    for bad in (dict(x=X + 8), dict(w=W + 4), dict(s=S + 1), dict(out=O + 2), dict(ws=WS + 8)):
+    for bad in (dict(x=X + 8), dict(w=W + 4), dict(s=S + 1), dict(out=O + 2), dict(T=40, ws=WS + 8), dict(x=None, ws=WS + 8)):
         assert _lin(fn, **bad) == -3, bad
-    for bad in (dict(out=X), dict(out=W), dict(out=S), dict(ws=X), dict(ws=O), dict(ws=W), dict(out=X + 16)):
+    for bad in (dict(out=X), dict(out=W), dict(out=S), dict(T=40, ws=X), dict(T=40, ws=O), dict(x=None, ws=W), dict(out=X + 16)):
         assert _lin(fn, **bad) == -4, bad
     assert _lin(fn, T=0, x=None, w=None, s=None, out=None, ws=None) == 0
     assert _lin(fn, T=1 << 20, K=1024) == -2  # 2 GiB of activations
     if fn == "w4_linear_add_mx":
-        assert _lin(fn, r=None) == -1 and _lin(fn, r=R + 8) == -3 and _lin(fn, r=O + 16) == -4 and _lin(fn, ws=R) == -4
+        assert _lin(fn, r=None) == -1 and _lin(fn, r=R + 8) == -3 and _lin(fn, r=O + 16) == -4 and _lin(fn, T=40, ws=R) == -4
 
 
 def test_quantize_and_dequantize_refusals():
@@ -244,3 +245,31 @@ def test_mx_tensor_views():
     q = w4.MXTensor(torch.arange(3 * (80 + 16), dtype=torch.uint8), 3, 160, 4)
     assert q.codes.shape == (3, 80) and q.scales.shape == (3, 5)
     assert q.codes[1, 0] == 80 and q.scales[1].tolist() == [(240 + 16 + i) % 256 for i in range(5)]
+
+
+def test_routes_and_workspace_of_every_shape():
+    """Every shape has a kernel; a workspace is asked for exactly where that is not the streaming one."""
+    for op in (0, 1, 2):
+        for fmt in (4, 8):
+            for K in (32, 512, 5120, 5152, 17408, 65536, 1 << 20):
+                for N in (16, 256, 5120, 12288):
+                    for T in (1, 2, 4, 5, 8, 16, 17, 32, 33, 64, 65, 100, 256, 1000, 4096):
+                        name, need = w4.mx_route_name(op, T, N, K, fmt), w4.linear_mx_workspace_bytes(op, T, N, K, fmt)
+                        assert need == (0 if name.startswith("mx_stream") else w4.mx_workspace_bytes(T, K, fmt))
+                        if op == 1:
+                            assert not name.startswith(("mx_stream_r1", "mx_stream_r3", "mx_ring_r1", "mx_ring_r3"))
+                        if fmt == 8:
+                            assert name != "mx_wide_320x256"
+                        if name.startswith("mx_ring") and T <= 64:
+                            assert int(name.rsplit("t", 1)[1]) == (16 if T <= 16 else 32 if T <= 32 else 64)
+    for bad in ((3, 1, 16, 32, 4), (0, 1, 24, 32, 4), (0, 1, 16, 48, 4), (0, -1, 16, 32, 4), (0, 1, 16, 32, 5)):
+        assert w4.mx_route_name(*bad) is None and w4.linear_mx_workspace_bytes(*bad) == 0
+
+
+@pytest.mark.parametrize("op,T,N,K,fmt,route", [
+    (0, 1, 12288, 5120, 8, "mx_stream_r3"), (0, 8, 12288, 5120, 8, "mx_stream_r3"), (0, 16, 12288, 5120, 8, "mx_ring_r3_t16"),
+    (1, 4, 17408, 5120, 8, "mx_stream_r2"), (1, 8, 17408, 5120, 8, "mx_ring_r2_t16"), (2, 2, 5120, 17408, 4, "mx_stream_r2"),
+    (2, 8, 5120, 17408, 4, "mx_ring_r2_t16"), (0, 64, 12288, 5120, 8, "mx_ring_r3_t64"), (0, 128, 12288, 5120, 8, "mx_wide_128x64"),
+    (2, 4096, 5120, 6144, 4, "mx_wide_320x256"), (1, 1024, 17408, 5120, 4, "mx_wide_320x256"), (0, 4096, 10240, 5120, 8, "mx_wide_256x128")])
+def test_route_choice_follows_the_measured_times(op, T, N, K, fmt, route):
+    assert w4.mx_route_name(op, T, N, K, fmt) == route

@@ -42,7 +42,7 @@ EXPORTS = (
     "w4_a8_workspace_bytes", "w4_quantize_a8", "w4_linear_a8", "w4_linear_swiglu_a8", "w4_linear_add_a8",
     "w4_dequantize_a8", "w4_mx_packed_bytes", "w4_mx_packed_scale_bytes", "w4_mx_workspace_bytes",
     "w4_mx_repack", "w4_mx_repack_pair", "w4_quantize_mx", "w4_dequantize_mx", "w4_linear_mx",
-    "w4_linear_swiglu_mx", "w4_linear_add_mx", "w4_rmsnorm", "w4_rmsnorm_a8", "w4_rmsnorm_mx",
+    "w4_linear_swiglu_mx", "w4_linear_add_mx", "w4_linear_mx_workspace_bytes", "w4_mx_route_name", "w4_rmsnorm", "w4_rmsnorm_a8", "w4_rmsnorm_mx",
 )
 
 MXFP4, MXFP8 = 4, 8  # W4_MXFP4, W4_MXFP8: element formats of the microscaled calls
@@ -136,9 +136,11 @@ def lib() -> ctypes.CDLL:
     L.w4_linear_add_a8.restype = i
     i64, f = ctypes.c_int64, ctypes.c_float
     for name, args in (("w4_mx_packed_bytes", [i, i]), ("w4_mx_packed_scale_bytes", [i, i]),
-                       ("w4_mx_workspace_bytes", [i, i, i])):
+                       ("w4_mx_workspace_bytes", [i, i, i]), ("w4_linear_mx_workspace_bytes", [i, i, i, i, i])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = sz
+    L.w4_mx_route_name.argtypes = [i, i, i, i, i]
+    L.w4_mx_route_name.restype = ctypes.c_char_p
     for name, args in (
             ("w4_mx_repack", [vp, vp, i, i, vp, vp]), ("w4_mx_repack_pair", [vp, vp, vp, vp, i, i, vp, vp]),
             ("w4_quantize_mx", [vp, i64, i, i, i, i, vp, sz, vp]),
@@ -682,54 +684,83 @@ def pack_mx_pair(gate, up, device="cuda") -> PackedMX:
                     gate[0].shape[1] * 2, True)
 
 
-def _on(device, stream, call):
-    """call(raw stream) with `device` current and `stream` (default: the device's current one) the
-    current stream, so that what the call allocates belongs to the stream that uses it."""
+# These calls are short (a few microseconds on the device), so the checks are written to cost little
+# when they pass: one condition for a good tensor, the detailed message only for a bad one.
+
+_torch = None
+_DTYPE = {}  # torch dtype -> W4_FP16 / W4_BF16
+
+
+def _load_torch():
+    global _torch
     import torch
-    if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return call(torch.cuda.current_stream(device).cuda_stream)
-        stream = torch.cuda.current_stream(device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+    _DTYPE.update({torch.float16: 0, torch.bfloat16: 1})
+    _torch = torch
+    return torch
+
+
+def _elsewhere(t, stream) -> bool:
+    """Whether a call on t needs another device or stream made current first."""
+    return stream is not None or (isinstance(t, _torch.Tensor) and t.is_cuda and
+                                  t.get_device() != _torch._C._cuda_getDevice())
+
+
+def _there(device, stream, call, *args, **kwargs):
+    """call(...) with `device` current and `stream` (default: the device's current one) its current
+    stream, so that what the call allocates belongs to the stream that uses it."""
+    if not isinstance(device, _torch.device) or device.type != "cuda":
+        raise ValueError("the tensors must be on a GPU")
+    with _torch.cuda.device(device), _torch.cuda.stream(stream):
+        return call(*args, **kwargs)
+
+
+def _device_of(x):
+    return getattr(x.workspace if isinstance(x, MXTensor) else x, "device", None)
+
+
+def _raw_stream(index: int) -> int:
+    return _torch._C._cuda_getCurrentRawStream(index)
 
 
 def _dtype16(dtype) -> int:
-    import torch
-    if dtype is torch.float16:
-        return 0
-    if dtype is torch.bfloat16:
-        return 1
-    raise ValueError(f"expected float16 or bfloat16, got {dtype}")
+    code = _DTYPE.get(dtype)
+    if code is None:
+        raise ValueError(f"expected float16 or bfloat16, got {dtype}")
+    return code
 
 
-def _check_rows(x, name: str) -> None:
-    """x: CUDA [T, K] in 16 bits, columns contiguous (rows may be further apart than K)."""
-    import torch
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
+def _rows(x, name: str):
+    """(T, K, dtype code, row stride) of x: CUDA [T, K] in 16 bits, columns contiguous (rows may be
+    further apart than K)."""
+    if not isinstance(x, _torch.Tensor) or not x.is_cuda or x.dim() != 2:
         raise ValueError(f"{name} must be a CUDA tensor of shape [T, K]")
-    _dtype16(x.dtype)
-    if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+    T, K = x.shape
+    ld, one = x.stride()
+    if (one != 1 and K > 1) or (ld < K and T > 1):
         raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    return T, K, _dtype16(x.dtype), ld if T > 1 else K
 
 
-def _row_stride(x) -> int:
-    return x.stride(0) if x.shape[0] > 1 else (x.shape[1] + 7) // 8 * 8
+def _is(t, name: str, shape, dtype, device: int) -> None:
+    """Raise unless t is a contiguous tensor of `dtype` and `shape` on GPU `device`."""
+    if not (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device and
+            t.is_contiguous()):
+        _check_tensor(t, name, shape, dtype, _torch.device("cuda", device))
 
 
 def _check_fmt(fmt: int) -> None:
-    if fmt not in (MXFP4, MXFP8):
+    if fmt != MXFP4 and fmt != MXFP8:
         raise ValueError(f"fmt must be MXFP4 ({MXFP4}) or MXFP8 ({MXFP8}), got {fmt!r}")
 
 
-def _bytes_on(workspace, need: int, device):
+def _bytes_on(workspace, need: int, device: int):
     """`workspace`, checked, or a new one of `need` bytes."""
-    import torch
+    torch = _torch
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    if not isinstance(workspace, torch.Tensor) or workspace.device != device or workspace.dtype != torch.uint8 or \
-            not workspace.is_contiguous() or workspace.numel() < need:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of >= {need} bytes on {device}")
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=f"cuda:{device}")
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != device or \
+            workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of >= {need} bytes on cuda:{device}")
     return workspace
 
 
@@ -737,119 +768,149 @@ def _mx_need(T: int, K: int, fmt: int) -> int:
     return T * (K * fmt // 8 + (K + 511) // 512 * 16)
 
 
-def _check_mx_tensor(q) -> None:
-    import torch
+def _check_mx_tensor(q) -> int:
+    """The GPU a quantised activation is on."""
+    if not isinstance(q, MXTensor):
+        raise ValueError("expected an MXTensor")
     _check_fmt(q.fmt)
-    if not isinstance(q.workspace, torch.Tensor) or not q.workspace.is_cuda:
+    if not isinstance(q.workspace, _torch.Tensor) or not q.workspace.is_cuda:
         raise ValueError("the quantised activations must be on a GPU")
-    _bytes_on(q.workspace, _mx_need(q.T, q.K, q.fmt), q.workspace.device)
+    if q.T < 0 or q.K <= 0 or q.K % 32:
+        raise ValueError(f"no quantised activations have T = {q.T}, K = {q.K}")
+    device = q.workspace.get_device()
+    _bytes_on(q.workspace, _mx_need(q.T, q.K, q.fmt), device)
+    return device
 
 
 def quantize_mx(x, fmt: int = MXFP4, workspace=None, stream=None) -> MXTensor:
-    """x (fp16 or bf16 [T, K], K a multiple of 32) -> MXTensor, via ``w4_quantize_mx``."""
-    _check_rows(x, "x")
+    """x (fp16 or bf16 [T, K], K a multiple of 32, rows may be strided) -> MXTensor, via
+    ``w4_quantize_mx``."""
+    _torch or _load_torch()
+    if _elsewhere(x, stream):
+        return _there(_device_of(x), stream, quantize_mx, x, fmt, workspace)
+    T, K, code, ld = _rows(x, "x")
     _check_fmt(fmt)
-    T, K = x.shape
-    if K % 32:
-        raise ValueError(f"K must be a multiple of 32, got {K}")
-
-    def call(raw):
-        ws = _bytes_on(workspace, _mx_need(T, K, fmt), x.device)
-        _check(lib().w4_quantize_mx(x.data_ptr(), _row_stride(x), T, K, fmt, _dtype16(x.dtype), ws.data_ptr(),
-                                    ws.numel(), raw), "w4_quantize_mx")
-        return MXTensor(ws, T, K, fmt)
-    return _on(x.device, stream, call)
+    if K % 32 or not K:
+        raise ValueError(f"K must be a positive multiple of 32, got {K}")
+    device = x.get_device()
+    ws = _bytes_on(workspace, _mx_need(T, K, fmt), device)
+    st = (_lib or lib()).w4_quantize_mx(x.data_ptr(), ld, T, K, fmt, code, ws.data_ptr(), ws.numel(),
+                                        _raw_stream(device))
+    if st:
+        raise W4Error(st, "w4_quantize_mx")
+    return MXTensor(ws, T, K, fmt)
 
 
 def dequantize_mx(q: MXTensor, dtype=None, out=None, stream=None):
     """MXTensor -> 16-bit [T, K] (dtype: torch.float16 unless given or `out` decides)."""
-    _check_mx_tensor(q)
-    return _dequantize(lambda *a: lib().w4_dequantize_mx(q.workspace.data_ptr(), q.workspace.numel(), q.T, q.K,
-                                                         q.fmt, *a), "w4_dequantize_mx", q.workspace, q.T, q.K,
-                       dtype, out, stream)
+    _torch or _load_torch()
+    device = _check_mx_tensor(q)
+    if _elsewhere(q.workspace, stream):
+        return _there(q.workspace.device, stream, dequantize_mx, q, dtype, out)
+    o, code = _out16(out, dtype, (q.T, q.K), device)
+    st = (_lib or lib()).w4_dequantize_mx(q.workspace.data_ptr(), q.workspace.numel(), q.T, q.K, q.fmt, code,
+                                          o.data_ptr(), _raw_stream(device))
+    if st:
+        raise W4Error(st, "w4_dequantize_mx")
+    return o
 
 
 def dequantize_a8(workspace, T: int, K: int, dtype=None, out=None, stream=None):
-    """A workspace of quantize_a8 or rmsnorm_a8 -> 16-bit [T, K]."""
-    import torch
+    """A workspace of quantize_a8 or rmsnorm_a8 -> 16-bit [T, K] (dtype as dequantize_mx)."""
+    torch = _torch or _load_torch()
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    nbytes = workspace.numel() * workspace.element_size()
-    return _dequantize(lambda *a: lib().w4_dequantize_a8(workspace.data_ptr(), nbytes, T, K, *a),
-                       "w4_dequantize_a8", workspace, T, K, dtype, out, stream)
+    if T < 0 or K <= 0 or K % 64:
+        raise ValueError(f"no A8 workspace has T = {T}, K = {K}")
+    if _elsewhere(workspace, stream):
+        return _there(workspace.device, stream, dequantize_a8, workspace, T, K, dtype, out)
+    device = workspace.get_device()
+    o, code = _out16(out, dtype, (T, K), device)
+    st = (_lib or lib()).w4_dequantize_a8(workspace.data_ptr(), workspace.numel() * workspace.element_size(), T, K,
+                                          code, o.data_ptr(), _raw_stream(device))
+    if st:
+        raise W4Error(st, "w4_dequantize_a8")
+    return o
 
 
-def _dequantize(fn, where, workspace, T, K, dtype, out, stream):
-    import torch
-    device = workspace.device
+def _out16(out, dtype, shape, device: int):
+    """(`out`, checked, or a new tensor; its dtype code)."""
+    torch = _torch
     if dtype is None:
         dtype = torch.float16 if out is None else out.dtype
     code = _dtype16(dtype)
-
-    def call(raw):
-        if out is None:
-            o = torch.empty((T, K), dtype=dtype, device=device)
-        else:
-            o = out
-            _check_tensor(o, "out", (T, K), dtype, device)
-        _check(fn(code, o.data_ptr(), raw), where)
-        return o
-    return _on(device, stream, call)
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}"), code
+    _is(out, "out", shape, dtype, device)
+    return out, code
 
 
 def _linear_mx(op: int, x, pw: PackedMX, residual, fmt, out, workspace, dtype, stream):
-    import torch
-    if (op == OP_SWIGLU) != pw.pair:
+    torch = _torch or _load_torch()
+    quantised = isinstance(x, MXTensor)
+    if _elsewhere(x.workspace if quantised else x, stream):
+        return _there(_device_of(x), stream, _linear_mx, op, x, pw, residual, fmt, out, workspace, dtype, None)
+    N, K, pair = pw.N, pw.K, pw.pair
+    if (op == OP_SWIGLU) != pair:
         raise ValueError("linear_swiglu_mx takes a gate/up pair from pack_mx_pair; the others a single matrix")
-    if isinstance(x, MXTensor):
-        _check_mx_tensor(x)
-        if x.K != pw.K:
-            raise ValueError(f"the quantised activations have K = {x.K}, the weights {pw.K}")
+    L = _lib or lib()
+    if quantised:
+        device = _check_mx_tensor(x)
+        if x.K != K:
+            raise ValueError(f"the quantised activations have K = {x.K}, the weights {K}")
         if workspace is not None or fmt not in (None, x.fmt):
             raise ValueError("quantised activations bring their own workspace and format")
-        T, fmt, workspace, device = x.T, x.fmt, x.workspace, x.workspace.device
+        T, fmt, ws, xp = x.T, x.fmt, x.workspace, None
         if dtype is None:
             dtype = out.dtype if out is not None else residual.dtype if residual is not None else torch.float16
-        xp = None
     else:
         if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
             raise ValueError("x must be a CUDA tensor of shape [T, K] or an MXTensor")
-        _check_tensor(x, "x", (x.shape[0], pw.K), x.dtype, x.device)
-        if dtype not in (None, x.dtype):
+        T, device = x.shape[0], x.get_device()
+        if x.shape[1] != K or not x.is_contiguous():
+            _check_tensor(x, "x", (T, K), x.dtype, x.device)
+        if dtype is not None and dtype is not x.dtype:
             raise ValueError("the output has the activations' dtype")
-        fmt = MXFP8 if fmt is None else fmt
+        if fmt is None:
+            fmt = MXFP8
         _check_fmt(fmt)
-        T, dtype, device, xp = x.shape[0], x.dtype, x.device, x.data_ptr()
+        dtype, xp = x.dtype, x.data_ptr()
     code = _dtype16(dtype)
-    rows, KB = (2 * pw.N if pw.pair else pw.N) // 16, (pw.K + 127) // 128
-    _check_tensor(pw.w, "packed codes", (rows * KB * 1024,), torch.uint8, device)
-    _check_tensor(pw.scales, "packed scales", (rows * KB * 64,), torch.uint8, device)
+    blocks = (2 * N if pair else N) // 16 * ((K + 127) // 128)
+    _is(pw.w, "packed codes", (blocks * 1024,), torch.uint8, device)
+    _is(pw.scales, "packed scales", (blocks * 64,), torch.uint8, device)
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype, device=pw.w.device)
+    else:
+        _is(out, "out", (T, N), dtype, device)
     if op == OP_ADD:
-        _check_tensor(residual, "residual", (T, pw.N), dtype, device)
-
-    def call(raw):
-        if out is None:
-            o = torch.empty((T, pw.N), dtype=dtype, device=device)
+        _is(residual, "residual", (T, N), dtype, device)
+    if quantised:
+        wp, wn = ws.data_ptr(), ws.numel()
+    else:
+        need = L.w4_linear_mx_workspace_bytes(op, T, N, K, fmt)
+        if workspace is None and need == 0:
+            wp, wn = None, 0
         else:
-            o = out
-            _check_tensor(o, "out", (T, pw.N), dtype, device)
-        ws = _bytes_on(workspace, _mx_need(T, pw.K, fmt), device)
-        L, head = lib(), (xp, pw.w.data_ptr(), pw.scales.data_ptr())
-        tail = (T, pw.N, pw.K, fmt, code, o.data_ptr(), ws.data_ptr(), ws.numel(), raw)
-        if op == OP_ADD:
-            _check(L.w4_linear_add_mx(*head, residual.data_ptr(), *tail), "w4_linear_add_mx")
-        elif op == OP_SWIGLU:
-            _check(L.w4_linear_swiglu_mx(*head, *tail), "w4_linear_swiglu_mx")
-        else:
-            _check(L.w4_linear_mx(*head, *tail), "w4_linear_mx")
-        return o
-    return _on(device, stream, call)
+            ws = _bytes_on(workspace, need, device)
+            wp, wn = ws.data_ptr(), ws.numel()
+    raw = _raw_stream(device)
+    if op == OP_ADD:
+        st = L.w4_linear_add_mx(xp, pw.w.data_ptr(), pw.scales.data_ptr(), residual.data_ptr(), T, N, K, fmt, code,
+                                out.data_ptr(), wp, wn, raw)
+    else:
+        st = (L.w4_linear_swiglu_mx if pair else L.w4_linear_mx)(
+            xp, pw.w.data_ptr(), pw.scales.data_ptr(), T, N, K, fmt, code, out.data_ptr(), wp, wn, raw)
+    if st:
+        raise W4Error(st, "w4_linear*_mx")
+    return out
 
 
 def linear_mx(x, pw: PackedMX, fmt=None, out=None, workspace=None, dtype=None, stream=None):
     """out[T, N] = x . W^T with MXFP4 weights, via ``w4_linear_mx``.  x: fp16 or bf16 [T, K], quantised
     to fmt (MXFP8 unless given) inside the call, or an MXTensor (from quantize_mx or rmsnorm_mx; then
-    dtype, torch.float16 unless given or `out` / the residual decides, is the output's type)."""
+    dtype, torch.float16 unless given or `out` / the residual decides, is the output's type).
+    workspace: uint8, >= linear_mx_workspace_bytes bytes (allocated here if None)."""
     return _linear_mx(OP_LINEAR, x, pw, None, fmt, out, workspace, dtype, stream)
 
 
@@ -863,68 +924,89 @@ def linear_add_mx(x, pw: PackedMX, residual, fmt=None, out=None, workspace=None,
     return _linear_mx(OP_ADD, x, pw, residual, fmt, out, workspace, dtype, stream)
 
 
+def linear_mx_workspace_bytes(op: int, T: int, N: int, K: int, fmt: int) -> int:
+    """Bytes of workspace a product on 16-bit activations needs (0: none)."""
+    return int(lib().w4_linear_mx_workspace_bytes(op, T, N, K, fmt))
+
+
+def mx_route_name(op: int, T: int, N: int, K: int, fmt: int) -> Optional[str]:
+    """The kernel a product of this shape runs (None for an invalid shape)."""
+    r = lib().w4_mx_route_name(op, T, N, K, fmt)
+    return None if r is None else r.decode()
+
+
 # ------------------------------------------------------------------ RMS norm
 
-def _rmsnorm(fn, where, x, weight, eps, residual, residual_out, k_multiple, stream, buffer):
-    """Shared checks; buffer() gives (the C call's trailing arguments, the result)."""
-    import torch
-    _check_rows(x, "x")
-    T, K = x.shape
+def _norm_args(x, weight, residual, residual_out, k_multiple: int):
+    """Checks shared by the norms: (T, K, dtype code, row stride, GPU, residual pointer, residual_out)."""
+    T, K, code, ld = _rows(x, "x")
     if K < 1 or K % k_multiple:
         raise ValueError(f"K must be a positive multiple of {k_multiple}, got {K}")
-    _check_tensor(weight, "weight", (K,), x.dtype, x.device)
-    if residual is not None:
-        _check_tensor(residual, "residual", (T, K), x.dtype, x.device)
+    device = x.get_device()
+    _is(weight, "weight", (K,), x.dtype, device)
+    if residual is None:
         if residual_out is not None:
-            _check_tensor(residual_out, "residual_out", (T, K), x.dtype, x.device)
-    elif residual_out is not None:
-        raise ValueError("residual_out without residual")
-
-    def call(raw):
-        h = residual_out
-        if residual is not None and h is None:
-            h = torch.empty((T, K), dtype=x.dtype, device=x.device)
-        mid, tail, result = buffer(T, K)
-        _check(fn()(x.data_ptr(), max(_row_stride(x), K) if T > 1 else K, _dptr(residual), weight.data_ptr(), eps, T,
-                    K, *mid, _dtype16(x.dtype), _dptr(h), *tail, raw), where)
-        return result, h
-    return _on(x.device, stream, call)
+            raise ValueError("residual_out without residual")
+        return T, K, code, ld, device, None, None
+    _is(residual, "residual", x.shape, x.dtype, device)
+    if residual_out is None:
+        residual_out = _torch.empty_like(residual)
+    else:
+        _is(residual_out, "residual_out", x.shape, x.dtype, device)
+    return T, K, code, ld, device, residual.data_ptr(), residual_out
 
 
 def rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out=None, stream=None):
     """(y, h): h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight per row of x [T, K] (fp16 or
     bf16, rows may be strided), via ``w4_rmsnorm``.  Without a residual h is None; residual_out may
     be residual (or a contiguous x), out either too."""
-    import torch
-
-    def buffer(T, K):
-        o = torch.empty((T, K), dtype=x.dtype, device=x.device) if out is None else out
-        _check_tensor(o, "out", (T, K), x.dtype, x.device)
-        return (), (o.data_ptr(),), o
-    return _rmsnorm(lambda: lib().w4_rmsnorm, "w4_rmsnorm", x, weight, eps, residual, residual_out, 1, stream, buffer)
+    _torch or _load_torch()
+    if _elsewhere(x, stream):
+        return _there(_device_of(x), stream, rmsnorm, x, weight, eps, residual, residual_out, out)
+    T, K, code, ld, device, rp, h = _norm_args(x, weight, residual, residual_out, 1)
+    if out is None:
+        out = _torch.empty((T, K), dtype=x.dtype, device=x.device)
+    else:
+        _is(out, "out", x.shape, x.dtype, device)
+    st = (_lib or lib()).w4_rmsnorm(x.data_ptr(), ld, rp, weight.data_ptr(), eps, T, K, code,
+                                    None if h is None else h.data_ptr(), out.data_ptr(), _raw_stream(device))
+    if st:
+        raise W4Error(st, "w4_rmsnorm")
+    return out, h
 
 
 def rmsnorm_a8(x, weight, eps: float = 1e-6, residual=None, residual_out=None, workspace=None, stream=None):
     """As rmsnorm with y quantised for the A8 calls: (workspace, h); linear_a8(None, pw,
     workspace=workspace, T=T) reads it.  K a multiple of 64."""
-    def buffer(T, K):
-        ws = _a8_workspace(workspace, T, K, x.device)
-        return (), (ws.data_ptr(), ws.numel() * ws.element_size()), ws
-    return _rmsnorm(lambda: lib().w4_rmsnorm_a8, "w4_rmsnorm_a8", x, weight, eps, residual, residual_out, 64, stream,
-                    buffer)
+    _torch or _load_torch()
+    if _elsewhere(x, stream):
+        return _there(_device_of(x), stream, rmsnorm_a8, x, weight, eps, residual, residual_out, workspace)
+    T, K, code, ld, device, rp, h = _norm_args(x, weight, residual, residual_out, 64)
+    ws = _a8_workspace(workspace, T, K, x.device)
+    st = (_lib or lib()).w4_rmsnorm_a8(x.data_ptr(), ld, rp, weight.data_ptr(), eps, T, K, code,
+                                       None if h is None else h.data_ptr(), ws.data_ptr(),
+                                       ws.numel() * ws.element_size(), _raw_stream(device))
+    if st:
+        raise W4Error(st, "w4_rmsnorm_a8")
+    return ws, h
 
 
 def rmsnorm_mx(x, weight, fmt: int = MXFP8, eps: float = 1e-6, residual=None, residual_out=None, workspace=None,
                stream=None):
     """As rmsnorm with y quantised to fmt: (MXTensor, h); linear_mx takes the MXTensor.  K a multiple
     of 32."""
+    _torch or _load_torch()
     _check_fmt(fmt)
-
-    def buffer(T, K):
-        ws = _bytes_on(workspace, _mx_need(T, K, fmt), x.device)
-        return (fmt,), (ws.data_ptr(), ws.numel()), MXTensor(ws, T, K, fmt)
-    return _rmsnorm(lambda: lib().w4_rmsnorm_mx, "w4_rmsnorm_mx", x, weight, eps, residual, residual_out, 32, stream,
-                    buffer)
+    if _elsewhere(x, stream):
+        return _there(_device_of(x), stream, rmsnorm_mx, x, weight, fmt, eps, residual, residual_out, workspace)
+    T, K, code, ld, device, rp, h = _norm_args(x, weight, residual, residual_out, 32)
+    ws = _bytes_on(workspace, _mx_need(T, K, fmt), device)
+    st = (_lib or lib()).w4_rmsnorm_mx(x.data_ptr(), ld, rp, weight.data_ptr(), eps, T, K, fmt, code,
+                                       None if h is None else h.data_ptr(), ws.data_ptr(), ws.numel(),
+                                       _raw_stream(device))
+    if st:
+        raise W4Error(st, "w4_rmsnorm_mx")
+    return MXTensor(ws, T, K, fmt), h
 
 
 # ------------------------------------------------------------------ per-verify-width graphs

@@ -104,6 +104,11 @@ Route pick(int op, int T, int rows, int K, int fmt) {
   return best;
 }
 
+bool product_ok(int op, int T, int N, int K, int fmt) {
+  return (op == W4_OP_LINEAR || op == W4_OP_SWIGLU || op == W4_OP_ADD) && fmt_ok(fmt) && mx_dims_ok(T, K) && N > 0 &&
+         N <= kMaxDim && N % w4layout::kRowTile == 0;
+}
+
 int run_linear_mx(int op, const uint16_t* x, const void* w, const uint8_t* scales, const uint16_t* res, int T, int N,
                   int K, int fmt, int dtype, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
   if (!fmt_ok(fmt) || !dtype_ok(dtype)) return W4_ERR_UNSUPPORTED;
@@ -120,17 +125,17 @@ int run_linear_mx(int op, const uint16_t* x, const void* w, const uint8_t* scale
   if (overlap(ro, span(x, xb)) || overlap(ro, span(w, wb)) || overlap(ro, span(scales, sb)) ||
       (res != out && overlap(ro, rr)))
     return W4_ERR_ALIAS;
-  int st = check_ws(ws, ws_bytes, w4::mx_workspace_bytes(T, K, fmt),
-                    {span(x, xb), ro, rr, span(w, wb), span(scales, sb)});
+  const Route route = pick(op, T, rows, K, fmt);
+  const bool fused = x && route.kind == STREAM;
+  int st = fused ? W4_OK : check_ws(ws, ws_bytes, w4::mx_workspace_bytes(T, K, fmt),
+                                    {span(x, xb), ro, rr, span(w, wb), span(scales, sb)});
   if (st != W4_OK) return st;
   st = w4::device_status();
   if (st != W4_OK) return st;
   const hipStream_t hs = static_cast<hipStream_t>(stream);
   uint8_t* codes = static_cast<uint8_t*>(ws);
-  uint8_t* xs = codes + w4::mx_scale_offset(T, K, fmt);
+  uint8_t* xs = codes ? codes + w4::mx_scale_offset(T, K, fmt) : nullptr;
   const bool bf16 = dtype == W4_BF16;
-  const Route route = pick(op, T, rows, K, fmt);
-  const bool fused = x && route.kind == STREAM;
   if (x && !fused && w4::launch_mx_quant(x, K, T, K, bf16, fmt, codes, xs, hs) != hipSuccess) return W4_ERR_LAUNCH;
   w4::MxArgs a;
   a.xq = codes;
@@ -197,6 +202,23 @@ int run_rmsnorm(int kind, const uint16_t* x, int64_t ldx, const uint16_t* res, c
 
 extern "C" size_t w4_mx_workspace_bytes(int T, int K, int fmt) {
   return mx_dims_ok(T, K) && fmt_ok(fmt) ? w4::mx_workspace_bytes(T, K, fmt) : 0;
+}
+
+extern "C" size_t w4_linear_mx_workspace_bytes(int op, int T, int N, int K, int fmt) {
+  if (!product_ok(op, T, N, K, fmt) || T == 0) return 0;
+  return pick(op, T, op == W4_OP_SWIGLU ? 2 * N : N, K, fmt).kind == STREAM ? 0 : w4::mx_workspace_bytes(T, K, fmt);
+}
+
+extern "C" const char* w4_mx_route_name(int op, int T, int N, int K, int fmt) {
+  if (!product_ok(op, T, N, K, fmt)) return nullptr;
+  static const char* const kStream[] = {"mx_stream_r1", "mx_stream_r2", "mx_stream_r3", "mx_stream_r4"};
+  static const char* const kRing[][4] = {{"mx_ring_r1_t16", "mx_ring_r2_t16", "mx_ring_r3_t16", "mx_ring_r4_t16"},
+                                         {"mx_ring_r1_t32", "mx_ring_r2_t32", "mx_ring_r3_t32", "mx_ring_r4_t32"},
+                                         {"mx_ring_r1_t64", "mx_ring_r2_t64", "mx_ring_r3_t64", "mx_ring_r4_t64"}};
+  static const char* const kWide[] = {"mx_wide_64x64", "mx_wide_128x64", "mx_wide_128x128", "mx_wide_256x128",
+                                      "mx_wide_320x256"};
+  const Route r = pick(op, T < 1 ? 1 : T, op == W4_OP_SWIGLU ? 2 * N : N, K, fmt);
+  return r.kind == STREAM ? kStream[r.rt - 1] : r.kind == RING ? kRing[r.tt == 4 ? 2 : r.tt - 1][r.rt - 1] : kWide[r.rt];
 }
 
 extern "C" int w4_quantize_mx(const uint16_t* x, int64_t ldx, int T, int K, int fmt, int dtype, void* workspace,
