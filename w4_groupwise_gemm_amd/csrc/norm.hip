@@ -19,21 +19,26 @@ using namespace w4mx;
 
 constexpr int kMaxWaves = 16;
 
-// The 8 columns at c of one row, or those of them below K (the others 0).  Rows of odd length or
-// stride start at any 2-byte address: memory access need not be aligned.
-template <bool BF>
-__device__ __forceinline__ void load8(const uint16_t* row, int c, int K, float (&f)[8]) {
+// The 8 columns at c of one row as 16-bit pairs, or those of them below K (the others 0).  Rows of odd
+// length or stride start at any 2-byte address: memory access need not be aligned.
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, int c, int K) {
+  u32x4 v = {0, 0, 0, 0};
   if (c + 8 <= K) {
-    u32x4 v;
     __builtin_memcpy(&v, row + c, 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = lo16<BF>(v[i]);
-      f[2 * i + 1] = hi16<BF>(v[i]);
-    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < K ? lo16<BF>(row[c + i]) : 0.f;
+    for (int i = 0; i < 8; ++i)
+      if (c + i < K) v[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
+  }
+  return v;
+}
+
+template <bool BF>
+__device__ __forceinline__ void widen(u32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = lo16<BF>(v[i]);
+    f[2 * i + 1] = hi16<BF>(v[i]);
   }
 }
 
@@ -51,12 +56,24 @@ __device__ __forceinline__ void store8(uint16_t* row, int c, int K, const float 
   }
 }
 
+// 8 columns of x and, where there is one, of the residual.
+struct Raw {
+  u32x4 x, r;
+};
+__device__ __forceinline__ Raw load_raw(const NormArgs& a, int t, int c) {
+  Raw v = {};
+  if (t < a.T && c < a.K) {
+    v.x = load8(a.x + t * a.ldx, c, a.K);
+    if (a.res) v.r = load8(a.res + (size_t)t * a.K, c, a.K);
+  }
+  return v;
+}
 template <bool BF>
-__device__ __forceinline__ void load_h(const NormArgs& a, int t, int c, float (&h)[8]) {
-  load8<BF>(a.x + t * a.ldx, c, a.K, h);
+__device__ __forceinline__ void sum_raw(const NormArgs& a, const Raw& v, float (&h)[8]) {
+  widen<BF>(v.x, h);
   if (a.res) {
     float r[8];
-    load8<BF>(a.res + (size_t)t * a.K, c, a.K, r);
+    widen<BF>(v.r, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] += r[i];
   }
@@ -80,10 +97,10 @@ __device__ __forceinline__ float row_rstd(float ss, float (*part)[kMaxWaves], in
 // y of the 8 columns at c, written in the output's form.  Every lane of the wave calls this (the
 // group maxima cross lanes); c >= K writes nothing.
 template <int KIND, bool BF>
-__device__ __forceinline__ void put8(const NormArgs& a, int t, int c, const float (&h)[8], float rstd) {
+__device__ __forceinline__ void put8(const NormArgs& a, int t, int c, const float (&h)[8], u32x4 weight, float rstd) {
   float y[8];
   if (c < a.K) {
-    load8<BF>(a.weight, c, a.K, y);
+    widen<BF>(weight, y);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] *= h[i] * rstd;
     if (a.res) store8<BF>(a.res_out + (size_t)t * a.K, c, a.K, h);
@@ -104,15 +121,24 @@ __device__ __forceinline__ void put8(const NormArgs& a, int t, int c, const floa
   if constexpr (KIND == NORM_A8) {
     m = max(m, (uint32_t)__shfl_xor((int)m, 4));
     if (c >= a.K) return;
-    // s = max / 127, q = rint(y / s), as the A8 route's own quantisation.  A group with an infinity
-    // or NaN has that as its scale, and codes of 1 where a 0 code would lose it.
-    const float s = __builtin_bit_cast(float, m) / 127.0f;
+    // s = max / 127, q = rint(y / s); y * (127 / max) is the quotient to a rounding, which moves a code only
+    // where y / s is that near a half, and saves seven divisions.  (Tiny groups, whose reciprocal would
+    // overflow, divide.)  A group with an infinity or NaN has that as its scale, and codes of 1 where a 0
+    // code would lose it.
+    const float top = __builtin_bit_cast(float, m), s = top / 127.0f;
     uint32_t q[8];
+    if (top > 1e-30f) {
+      const float inv = 127.0f / top;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = s > 0.f ? rintf(y[i] / s) : 0.f;
-      v = m >= 0x7F800000u ? 1.f : fminf(fmaxf(v, -127.f), 127.f);
-      q[i] = (uint32_t)(int)v & 0xFFu;
+      for (int i = 0; i < 8; ++i) q[i] = (uint32_t)(int)fminf(fmaxf(rintf(y[i] * inv), -127.f), 127.f) & 0xFFu;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        q[i] = s > 0.f ? (uint32_t)(int)fminf(fmaxf(rintf(y[i] / s), -127.f), 127.f) & 0xFFu : 0u;
+    }
+    if (m >= 0x7F800000u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = 1u;
     }
     int8_t* dst = static_cast<int8_t*>(a.codes) + (size_t)t * a.K + c;
     *reinterpret_cast<u32x2*>(dst) = u32x2{q[0] | (q[4] << 8) | (q[1] << 16) | (q[5] << 24),
@@ -147,26 +173,35 @@ __device__ __forceinline__ void put8(const NormArgs& a, int t, int c, const floa
   }
 }
 
-// VPT vectors of 8 columns per lane in registers.
+constexpr int max_threads(int vpt) { return vpt <= 2 ? 1024 : vpt == 4 ? 640 : 512; }  // (registers)
+
+// VPT vectors of 8 columns per lane in registers.  A workgroup takes rows blockIdx.x, + gridDim.x, ..: the
+// next row's loads are issued before this row's sum, and the weight stays in registers.
 template <int KIND, bool BF, int VPT>
-__global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(max_threads(VPT)) void norm_kernel(NormArgs a) {
   __shared__ float part[2][kMaxWaves];
+  const int c0 = threadIdx.x * 8, dc = blockDim.x * 8;
+  u32x4 weight[VPT];
+  Raw next[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) next[v] = load_raw(a, blockIdx.x, c0 + v * dc);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) weight[v] = c0 + v * dc < a.K ? load8(a.weight, c0 + v * dc, a.K) : u32x4{0, 0, 0, 0};
   int slot = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, slot ^= 1) {
     float h[VPT][8];
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * 8;
-      if (c < a.K) {
-        load_h<BF>(a, t, c, h[v]);
+      sum_raw<BF>(a, next[v], h[v]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
-      }
+      for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
     }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) next[v] = load_raw(a, t + gridDim.x, c0 + v * dc);
     const float rstd = row_rstd(ss, part, slot, a);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) put8<KIND, BF>(a, t, (v * blockDim.x + threadIdx.x) * 8, h[v], rstd);
+    for (int v = 0; v < VPT; ++v) put8<KIND, BF>(a, t, c0 + v * dc, h[v], weight[v], rstd);
   }
 }
 
@@ -180,30 +215,39 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     float ss = 0.f;
     for (int c = threadIdx.x * 8; c < a.K; c += blockDim.x * 8) {
       float h[8];
-      load_h<BF>(a, t, c, h);
+      sum_raw<BF>(a, load_raw(a, t, c), h);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(h[i], h[i], ss);
     }
     const float rstd = row_rstd(ss, part, slot, a);
     for (int c0 = 0; c0 < a.K; c0 += blockDim.x * 8) {
       const int c = c0 + threadIdx.x * 8;
-      float h[8] = {};
-      if (c < a.K) load_h<BF>(a, t, c, h);
-      put8<KIND, BF>(a, t, c, h, rstd);
+      float h[8];
+      sum_raw<BF>(a, load_raw(a, t, c), h);
+      put8<KIND, BF>(a, t, c, h, c < a.K ? load8(a.weight, c, a.K) : u32x4{0, 0, 0, 0}, rstd);
     }
   }
 }
 
-constexpr int kMaxGrid = 1 << 20;  // workgroups; further rows are taken in turn
+constexpr int kCUs = 256;
 
+// Threads and vectors per lane.  Few rows: as many lanes as the row has vectors, for latency.  Many rows:
+// at most 320 lanes (4096 x 5120 with the residual, 16-bit output: 34.0 us; 640 lanes of one vector
+// 36.4, 192 lanes of four 38.0), so that a compute unit has more rows on their way, and two rows or
+// more per workgroup (one where a lane holds four vectors or more: 4096 x 17408 114 us against 122).
 template <int KIND, bool BF>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
-  const dim3 grid(a.T < kMaxGrid ? a.T : kMaxGrid);
   const int64_t nvec = ((int64_t)a.K + 7) / 8;
-  const int vpt = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4;
-  if (nvec > 4 * 1024) return launch_kernel(&norm_long_kernel<KIND, BF>, grid, dim3(1024), 0, stream, a);
-  const int threads = (int)(((nvec + vpt - 1) / vpt + 63) / 64 * 64);
-  auto k = vpt == 1 ? &norm_kernel<KIND, BF, 1> : vpt == 2 ? &norm_kernel<KIND, BF, 2> : &norm_kernel<KIND, BF, 4>;
+  int vpt = 1;
+  while (vpt < 8 && nvec > (int64_t)vpt * (a.T <= 2 * kCUs ? max_threads(vpt) : 320)) vpt *= 2;
+  const int64_t threads = ((nvec + vpt - 1) / vpt + 63) / 64 * 64;
+  const int resident = kCUs * (threads >= 1024 ? 2 : (int)(2048 / threads));
+  const int most = resident * (vpt >= 4 ? 1 : 2);
+  const dim3 grid(a.T < most ? a.T : most);
+  if (threads > max_threads(vpt))
+    return launch_kernel(&norm_long_kernel<KIND, BF>, grid, dim3(1024), 0, stream, a);
+  auto k = vpt == 1 ? &norm_kernel<KIND, BF, 1> : vpt == 2 ? &norm_kernel<KIND, BF, 2>
+         : vpt == 4 ? &norm_kernel<KIND, BF, 4> : &norm_kernel<KIND, BF, 8>;
   return launch_kernel(k, grid, dim3(threads), 0, stream, a);
 }
 
