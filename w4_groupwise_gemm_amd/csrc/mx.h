@@ -42,6 +42,7 @@ struct NormArgs {
   void* codes;             // quantised output
   void* scales;
   int64_t ldx;
+  double inv_k;            // 1 / K
   float eps;
   int T, K;
 };

@@ -192,6 +192,7 @@ int run_rmsnorm(int kind, const uint16_t* x, int64_t ldx, const uint16_t* res, c
   a.codes = ws;
   a.scales = need ? static_cast<char*>(ws) + scale_offset : nullptr;
   a.ldx = ldx;
+  a.inv_k = 1.0 / K;
   a.eps = eps;
   a.T = T;
   a.K = K;

@@ -79,19 +79,30 @@ __device__ __forceinline__ void sum_raw(const NormArgs& a, const Raw& v, float (
   }
 }
 
-// 1 / sqrt(mean + eps) from every thread's share of the sum of squares.  Two slots of partial sums
-// alternate between rows, so one barrier a row is enough.
-__device__ __forceinline__ float row_rstd(float ss, float (*part)[kMaxWaves], int slot, const NormArgs& a) {
+// A thread's share of the sum of squares, and 1 / sqrt(mean + eps) from the shares.  Sums of 8 squares are
+// formed in fp32 (their roundings average out over a row) and everything after them in fp64: an
+// error in this one factor moves every y of the row the same way, and 8-bit codes with them.  (All of it
+// in fp64, with its division and root, took 10 % longer at 4096 x 5120.)  Two slots of partial sums alternate between rows, so one
+// barrier a row is enough.
+__device__ __forceinline__ double add_squares(double ss, const float (&h)[8]) {
+  const float a = fmaf(h[0], h[0], h[1] * h[1]) + fmaf(h[2], h[2], h[3] * h[3]);
+  const float b = fmaf(h[4], h[4], h[5] * h[5]) + fmaf(h[6], h[6], h[7] * h[7]);
+  return ss + (double)(a + b);
+}
+__device__ __forceinline__ float row_rstd(double ss, double (*part)[kMaxWaves], int slot, const NormArgs& a) {
 #pragma unroll
   for (int o = 32; o; o >>= 1) ss += __shfl_xor(ss, o);
   const int waves = blockDim.x >> 6;
   if (waves > 1) {
     if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = ss;
     __syncthreads();
-    ss = 0.f;
+    ss = 0.;
     for (int i = 0; i < waves; ++i) ss += part[slot][i];
   }
-  return 1.0f / sqrtf(ss / (float)a.K + a.eps);
+  const double v = fma(ss, a.inv_k, (double)a.eps);
+  // one Newton step in fp64 on the fp32 root (its error squared: below 2^-40)
+  const float y = rsqrtf((float)v);
+  return y > 0.f && y < __builtin_inff() ? (float)((double)y * fma(-0.5 * v * y, (double)y, 1.5)) : y;
 }
 
 // y of the 8 columns at c, written in the output's form.  Every lane of the wave calls this (the
@@ -102,7 +113,7 @@ __device__ __forceinline__ void put8(const NormArgs& a, int t, int c, const floa
   if (c < a.K) {
     widen<BF>(weight, y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] *= h[i] * rstd;
+    for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * y[i];
     if (a.res) store8<BF>(a.res_out + (size_t)t * a.K, c, a.K, h);
   } else {
 #pragma unroll
@@ -175,33 +186,41 @@ __device__ __forceinline__ void put8(const NormArgs& a, int t, int c, const floa
 
 constexpr int max_threads(int vpt) { return vpt <= 2 ? 1024 : vpt == 4 ? 640 : 512; }  // (registers)
 
+constexpr int min_waves(int vpt) { return vpt == 1 ? 7 : vpt == 2 ? 6 : vpt == 4 ? 3 : 2; }  // per SIMD
+
 // VPT vectors of 8 columns per lane in registers.  A workgroup takes rows blockIdx.x, + gridDim.x, ..: the
-// next row's loads are issued before this row's sum, and the weight stays in registers.
+// next row's loads are issued before this row's sum.  Long rows (VPT >= 4) keep the weight in registers
+// (4096 x 17408: 114 us, read again for each row 134); for short ones the waves that those registers
+// cost are worth more (4096 x 5120 without residual: 21.1 us read again, 23.3 kept).
 template <int KIND, bool BF, int VPT>
-__global__ __launch_bounds__(max_threads(VPT)) void norm_kernel(NormArgs a) {
-  __shared__ float part[2][kMaxWaves];
+__global__ __launch_bounds__(max_threads(VPT), min_waves(VPT)) void norm_kernel(NormArgs a) {
+  __shared__ double part[2][kMaxWaves];
   const int c0 = threadIdx.x * 8, dc = blockDim.x * 8;
-  u32x4 weight[VPT];
+  constexpr bool kKeep = VPT >= 4;
+  u32x4 weight[kKeep ? VPT : 1];
+  auto load_weight = [&](int c) { return c < a.K ? load8(a.weight, c, a.K) : u32x4{0, 0, 0, 0}; };
   Raw next[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) next[v] = load_raw(a, blockIdx.x, c0 + v * dc);
+  if constexpr (kKeep) {
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) weight[v] = c0 + v * dc < a.K ? load8(a.weight, c0 + v * dc, a.K) : u32x4{0, 0, 0, 0};
+    for (int v = 0; v < VPT; ++v) weight[v] = load_weight(c0 + v * dc);
+  }
   int slot = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, slot ^= 1) {
     float h[VPT][8];
-    float ss = 0.f;
+    double ss = 0.;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       sum_raw<BF>(a, next[v], h[v]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
+      ss = add_squares(ss, h[v]);
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) next[v] = load_raw(a, t + gridDim.x, c0 + v * dc);
     const float rstd = row_rstd(ss, part, slot, a);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) put8<KIND, BF>(a, t, c0 + v * dc, h[v], weight[v], rstd);
+    for (int v = 0; v < VPT; ++v)
+      put8<KIND, BF>(a, t, c0 + v * dc, h[v], kKeep ? weight[kKeep ? v : 0] : load_weight(c0 + v * dc), rstd);
   }
 }
 
@@ -209,15 +228,14 @@ __global__ __launch_bounds__(max_threads(VPT)) void norm_kernel(NormArgs a) {
 // before it writes them, so the outputs may still be the inputs).
 template <int KIND, bool BF>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
-  __shared__ float part[2][kMaxWaves];
+  __shared__ double part[2][kMaxWaves];
   int slot = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, slot ^= 1) {
-    float ss = 0.f;
+    double ss = 0.;
     for (int c = threadIdx.x * 8; c < a.K; c += blockDim.x * 8) {
       float h[8];
       sum_raw<BF>(a, load_raw(a, t, c), h);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(h[i], h[i], ss);
+      ss = add_squares(ss, h);
     }
     const float rstd = row_rstd(ss, part, slot, a);
     for (int c0 = 0; c0 < a.K; c0 += blockDim.x * 8) {
@@ -232,8 +250,8 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 constexpr int kCUs = 256;
 
 // Threads and vectors per lane.  Few rows: as many lanes as the row has vectors, for latency.  Many rows:
-// at most 320 lanes (4096 x 5120 with the residual, 16-bit output: 34.0 us; 640 lanes of one vector
-// 36.4, 192 lanes of four 38.0), so that a compute unit has more rows on their way, and two rows or
+// at most 320 lanes (4096 x 5120 with the residual, 16-bit output: 35.8 us; 640 lanes of one vector
+// 38.0, 192 lanes of four 39.8), so that a compute unit has more rows on their way, and two rows or
 // more per workgroup (one where a lane holds four vectors or more: 4096 x 17408 114 us against 122).
 template <int KIND, bool BF>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
