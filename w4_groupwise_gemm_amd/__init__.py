@@ -606,6 +606,9 @@ class PackedMX:
     N: int             # output width (of each of gate/up for a pair)
     K: int
     pair: bool = False
+    # what the calls have worked out: the tensors found to fit, and workspace sizes by (T, fmt)
+    _fits: tuple = dataclasses.field(default=(), init=False, repr=False, compare=False)
+    _need: dict = dataclasses.field(default_factory=dict, init=False, repr=False, compare=False)
 
     @property
     def nbytes_stream(self) -> int:
@@ -850,7 +853,7 @@ def _linear_mx(op: int, x, pw: PackedMX, residual, fmt, out, workspace, dtype, s
     quantised = isinstance(x, MXTensor)
     if _elsewhere(x.workspace if quantised else x, stream):
         return _there(_device_of(x), stream, _linear_mx, op, x, pw, residual, fmt, out, workspace, dtype, None)
-    N, K, pair = pw.N, pw.K, pw.pair
+    N, K, pair, w, scales = pw.N, pw.K, pw.pair, pw.w, pw.scales
     if (op == OP_SWIGLU) != pair:
         raise ValueError("linear_swiglu_mx takes a gate/up pair from pack_mx_pair; the others a single matrix")
     L = _lib or lib()
@@ -876,11 +879,15 @@ def _linear_mx(op: int, x, pw: PackedMX, residual, fmt, out, workspace, dtype, s
         _check_fmt(fmt)
         dtype, xp = x.dtype, x.data_ptr()
     code = _dtype16(dtype)
-    blocks = (2 * N if pair else N) // 16 * ((K + 127) // 128)
-    _is(pw.w, "packed codes", (blocks * 1024,), torch.uint8, device)
-    _is(pw.scales, "packed scales", (blocks * 64,), torch.uint8, device)
+    fits = pw._fits
+    if not (fits and fits[0] is w and fits[1] is scales and fits[2:] == (N, K, pair, device)):
+        blocks = (2 * N if pair else N) // 16 * ((K + 127) // 128)
+        _is(w, "packed codes", (blocks * 1024,), torch.uint8, device)
+        _is(scales, "packed scales", (blocks * 64,), torch.uint8, device)
+        pw._fits = (w, scales, N, K, pair, device)
+        pw._need = {}
     if out is None:
-        out = torch.empty((T, N), dtype=dtype, device=pw.w.device)
+        out = w.new_empty((T, N), dtype=dtype) if quantised else x.new_empty((T, N))
     else:
         _is(out, "out", (T, N), dtype, device)
     if op == OP_ADD:
@@ -888,7 +895,11 @@ def _linear_mx(op: int, x, pw: PackedMX, residual, fmt, out, workspace, dtype, s
     if quantised:
         wp, wn = ws.data_ptr(), ws.numel()
     else:
-        need = L.w4_linear_mx_workspace_bytes(op, T, N, K, fmt)
+        need = pw._need.get((T, fmt))
+        if need is None:
+            need = L.w4_linear_mx_workspace_bytes(op, T, N, K, fmt)
+            if len(pw._need) < 4096:
+                pw._need[T, fmt] = need
         if workspace is None and need == 0:
             wp, wn = None, 0
         else:
@@ -896,11 +907,11 @@ def _linear_mx(op: int, x, pw: PackedMX, residual, fmt, out, workspace, dtype, s
             wp, wn = ws.data_ptr(), ws.numel()
     raw = _raw_stream(device)
     if op == OP_ADD:
-        st = L.w4_linear_add_mx(xp, pw.w.data_ptr(), pw.scales.data_ptr(), residual.data_ptr(), T, N, K, fmt, code,
+        st = L.w4_linear_add_mx(xp, w.data_ptr(), scales.data_ptr(), residual.data_ptr(), T, N, K, fmt, code,
                                 out.data_ptr(), wp, wn, raw)
     else:
         st = (L.w4_linear_swiglu_mx if pair else L.w4_linear_mx)(
-            xp, pw.w.data_ptr(), pw.scales.data_ptr(), T, N, K, fmt, code, out.data_ptr(), wp, wn, raw)
+            xp, w.data_ptr(), scales.data_ptr(), T, N, K, fmt, code, out.data_ptr(), wp, wn, raw)
     if st:
         raise W4Error(st, "w4_linear*_mx")
     return out
@@ -965,7 +976,7 @@ def rmsnorm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out=
         return _there(_device_of(x), stream, rmsnorm, x, weight, eps, residual, residual_out, out)
     T, K, code, ld, device, rp, h = _norm_args(x, weight, residual, residual_out, 1)
     if out is None:
-        out = _torch.empty((T, K), dtype=x.dtype, device=x.device)
+        out = x.new_empty((T, K)) if h is None else _torch.empty_like(h)
     else:
         _is(out, "out", x.shape, x.dtype, device)
     st = (_lib or lib()).w4_rmsnorm(x.data_ptr(), ld, rp, weight.data_ptr(), eps, T, K, code,
