@@ -35,6 +35,7 @@ CASES = [
     ("linear", 200, 12304, 416, 4, "mx_wide_128x128"), ("swiglu", 65, 12304, 288, 8, "mx_wide_128x128"), ("add", 200, 12304, 1184, 8, "mx_wide_128x128"),
     ("add", 500, 12304, 288, 8, "mx_wide_256x128"), ("linear", 1000, 12304, 160, 4, "mx_wide_256x128"), ("swiglu", 257, 17424, 672, 4, "mx_wide_256x128"),
     ("add", 4100, 4112, 160, 4, "mx_wide_320x256"), ("swiglu", 1000, 8208, 416, 4, "mx_wide_320x256"), ("linear", 4100, 4112, 1184, 4, "mx_wide_320x256"),
+    ("add", 1, 1040, 51200, 8, "mx_stream_r1"),  # over 64 KB of LDS
     ("linear", 40, 48, 131072, 8, "mx_wide_64x64"), ("linear", 5, 32, 524288, 4, "mx_wide_64x64"),  # rows too long for the ring's LDS
 ]
 

@@ -121,6 +121,44 @@ def test_many_rows():
     check_rounded(h, wh, torch.bfloat16, 2.0 ** -24)
 
 
+def test_more_rows_than_a_grid_dimension():
+    T, K = 70001, 64
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn(T, K, device=DEV, generator=g).half()
+    w = torch.ones(K, device=DEV).half()
+    y, _ = w4.rmsnorm(x, w)
+    q, _ = w4.rmsnorm_mx(x, w)
+    d = w4.dequantize_mx(q)
+    rows = torch.tensor([0, 1, 65535, 65536, 65537, T - 1], device=DEV)
+    y6, _ = w4.rmsnorm(x[rows], w)
+    q6, _ = w4.rmsnorm_mx(x[rows], w)
+    assert torch.equal(y[rows], y6) and torch.equal(q.codes[rows], q6.codes) and torch.equal(q.scales[rows], q6.scales)
+    assert torch.equal(d[rows], w4.dequantize_mx(q6))
+    assert torch.equal(w4.quantize_mx(x).codes[rows], w4.quantize_mx(x[rows]).codes)
+    ws, _ = w4.rmsnorm_a8(x, w)
+    ws6, _ = w4.rmsnorm_a8(x[rows], w)
+    assert torch.equal(w4.dequantize_a8(ws, T, K)[rows], w4.dequantize_a8(ws6, 6, K))
+
+
+def test_on_another_stream():
+    x, r, w = inputs(33, 5120, torch.float16)
+    want = [w4.rmsnorm(x, w, residual=r), w4.rmsnorm_mx(x, w, residual=r), w4.rmsnorm_a8(x, w, residual=r)]
+    wq = w4.quantize_mx(x)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    y, h = w4.rmsnorm(x, w, residual=r, stream=s)
+    q, _ = w4.rmsnorm_mx(x, w, residual=r, stream=s)
+    ws, _ = w4.rmsnorm_a8(x, w, residual=r, stream=s)
+    xq = w4.quantize_mx(x, stream=s)
+    d = w4.dequantize_mx(xq, stream=s)
+    e = w4.dequantize_a8(ws, 33, 5120, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want[0][0]) and torch.equal(h, want[0][1])
+    assert torch.equal(q.codes, want[1][0].codes) and torch.equal(q.scales, want[1][0].scales)
+    assert torch.equal(xq.codes, wq.codes) and torch.equal(d, w4.dequantize_mx(wq))
+    assert torch.equal(e, w4.dequantize_a8(want[2][0], 33, 5120))
+
+
 @pytest.mark.parametrize("K,stride,off", [(288, 1024, 256), (257, 1001, 8), (256, 259, 0)])
 def test_strided_rows(K, stride, off):
     g = torch.Generator().manual_seed(K)

@@ -22,7 +22,7 @@ __device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t r, char* lds, in
 __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t r, int from, char* lds, int bytes, int wave,
                                             int waves, int lane) {
   for (int i = wave * 1024; i < bytes; i += waves * 1024)
-    to_lds16(r, lds + i, i + lane * 16 < bytes ? from + lane * 16 : kOut, i);
+    to_lds16(r, lds + i, i + lane * 16 < bytes ? from + i + lane * 16 : kOut, 0);
 }
 // LDS taken by such a copy: whole loads.
 constexpr size_t lds_copy(size_t bytes) { return (bytes + 1023) / 1024 * 1024; }
@@ -162,7 +162,8 @@ __global__ __launch_bounds__(64 * NW) void mx_stream_kernel(MxArgs a, int tp_log
     fetch(it, o);
     put(it, o);
   }
-  wait_vmcnt<DW * RT>();  // the scale bytes
+  asm volatile("" ::: "memory");  // (the weights' loads stay above the wait that counts them)
+  wait_vmcnt<DW * RT>();          // the scale bytes
   arrive_wait();
 
   f32x4 acc[RT][1] = {};
@@ -243,12 +244,14 @@ __global__ __launch_bounds__(64 * NW) void mx_ring_kernel(MxArgs a, int groups) 
   WUnit w[D];
 #pragma unroll
   for (int d = 0; d < D; ++d) load(wave + NW * d, ring + d * R::kX, w[d]);
+  asm volatile("" ::: "memory");  // (loads stay above the waits that count them, here and below)
   __builtin_amdgcn_sched_barrier(0);
   wait_vmcnt<D * R::kLoads>();  // the scale bytes
   arrive_wait();
   for (int u = wave; u < units; u += NW * D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
+      asm volatile("" ::: "memory");
       wait_vmcnt<(D - 1) * R::kLoads>();
       __builtin_amdgcn_sched_barrier(0);
       char* slot = ring + d * R::kX;

@@ -150,15 +150,16 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_k
     for (int i = 0; i < S::kCL; ++i)
       to_lds16(cr[i], st + min(wave + kWaves * i, S::kCN - 1) * 1024, last ? vlast[i] : voff[i], kb * step[i]);
   };
-  // (past the last columns: bytes that nothing reads)
-  auto load_scales = [&](int q) {
+  // (past the last columns the last ones again, which nothing reads)
+  auto load_scales = [&](int q, int last) {
 #pragma unroll
     for (int i = 0; i < S::kSL; ++i)
-      to_lds16(sr[i], scales + (q & 1) * S::kScales + min(wave + kWaves * i, S::kSN - 1) * 1024, soff[i], q * sstep[i]);
+      to_lds16(sr[i], scales + (q & 1) * S::kScales + min(wave + kWaves * i, S::kSN - 1) * 1024, soff[i],
+               min(q, last) * sstep[i]);
   };
 
   f32x16 acc[MT][NT] = {};
-  load_scales(0);
+  load_scales(0, 0);
 #pragma unroll
   for (int s = 0; s < S::kStages - 1; ++s) load(min(s, a.KB - 1), smem + s * S::kCodes);
   int slot = 0, fill = S::kStages - 1;
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_k
     arrive_wait();
     load(min(kb + S::kStages - 1, a.KB - 1), smem + fill * S::kCodes);
     // (the buffer's previous bytes were last read at least one stage ago)
-    if constexpr ((P + S::kStages - 1) % 4 == 3) load_scales((kb + S::kStages) / 4);
+    if constexpr ((P + S::kStages - 1) % 4 == 3) load_scales((kb + S::kStages) / 4, (a.KB - 1) / 4);
     fill = fill == S::kStages - 1 ? 0 : fill + 1;
     const char* st = smem + slot * S::kCodes;
     slot = slot == S::kStages - 1 ? 0 : slot + 1;
