@@ -21,9 +21,20 @@ CASES = [
     ("linear", 2, 4112, 2080, 8, "mx_stream_r2"), ("swiglu", 5, 1040, 1184, 4, "mx_stream_r2"), ("swiglu", 13, 16, 160, 8, "mx_stream_r2"),
     ("linear", 1, 8208, 5152, 8, "mx_stream_r3"), ("add", 7, 8208, 1184, 4, "mx_stream_r3"),
     ("linear", 2, 12304, 672, 4, "mx_stream_r4"), ("swiglu", 3, 4112, 2080, 8, "mx_stream_r4"),
+    ("add", 3, 17424, 672, 8, "mx_stream_r5"), ("swiglu", 6, 8208, 672, 4, "mx_stream_r6"),
+    ("swiglu", 9, 12304, 160, 8, "mx_stream_r8"), ("swiglu", 2, 17424, 1184, 4, "mx_stream_r10"), ("swiglu", 7, 17424, 416, 8, "mx_stream_r10"),
     ("add", 16, 48, 8224, 4, "mx_ring_r1_t16"), ("linear", 9, 528, 33024, 8, "mx_ring_r1_t16"),
     ("linear", 16, 4112, 5152, 8, "mx_ring_r2_t16"), ("swiglu", 12, 80, 8224, 4, "mx_ring_r2_t16"),
     ("add", 16, 8208, 5152, 8, "mx_ring_r3_t16"), ("linear", 16, 12304, 5152, 4, "mx_ring_r4_t16"), ("swiglu", 16, 4112, 5152, 8, "mx_ring_r4_t16"),
+    ("linear", 12, 17424, 5152, 4, "mx_ring_r5_t16"), ("swiglu", 12, 8208, 5152, 8, "mx_ring_r6_t16"),
+    ("swiglu", 15, 12304, 5152, 4, "mx_ring_r8_t16"), ("swiglu", 13, 17424, 5152, 8, "mx_ring_r10_t16"),
+    ("swiglu", 16, 17424, 5152, 4, "mx_ring_r10_t16"),
+    ("add", 21, 17424, 1184, 8, "mx_ring_r5_t32"), ("swiglu", 32, 8208, 2080, 4, "mx_ring_r6_t32"),
+    ("swiglu", 18, 12304, 672, 4, "mx_ring_r8_t32"), ("swiglu", 31, 17424, 1184, 8, "mx_ring_r10_t32"),
+    ("swiglu", 24, 17424, 672, 4, "mx_ring_r10_t32"),
+    ("linear", 63, 17424, 1184, 4, "mx_ring_r5_t64"), ("swiglu", 45, 8208, 1184, 8, "mx_ring_r6_t64"),
+    ("swiglu", 64, 12304, 672, 8, "mx_ring_r8_t64"), ("swiglu", 49, 17424, 2080, 4, "mx_ring_r10_t64"),
+    ("swiglu", 60, 17424, 1184, 8, "mx_ring_r10_t64"),
     ("linear", 17, 16, 160, 8, "mx_ring_r1_t32"), ("add", 30, 528, 5152, 4, "mx_ring_r1_t32"),
     ("linear", 32, 4112, 2080, 4, "mx_ring_r2_t32"), ("swiglu", 25, 272, 1184, 8, "mx_ring_r2_t32"),
     ("add", 31, 8208, 1184, 8, "mx_ring_r3_t32"), ("linear", 19, 12304, 672, 4, "mx_ring_r4_t32"), ("swiglu", 28, 4112, 672, 8, "mx_ring_r4_t32"),
@@ -31,7 +42,7 @@ CASES = [
     ("linear", 63, 4112, 1184, 8, "mx_ring_r2_t64"), ("swiglu", 40, 1040, 2080, 4, "mx_ring_r2_t64"), ("add", 65, 2064, 672, 8, "mx_ring_r2_t64"),
     ("add", 64, 8208, 2080, 4, "mx_ring_r3_t64"), ("linear", 50, 12304, 672, 8, "mx_ring_r4_t64"), ("swiglu", 37, 4112, 1184, 8, "mx_ring_r4_t64"),
     ("linear", 65, 4112, 1184, 8, "mx_wide_64x64"), ("swiglu", 70, 2064, 160, 4, "mx_wide_64x64"), ("add", 90, 4112, 2080, 4, "mx_wide_64x64"),
-    ("add", 65, 8208, 672, 8, "mx_wide_128x64"), ("swiglu", 65, 4112, 544, 4, "mx_wide_128x64"),
+    ("add", 65, 8208, 672, 8, "mx_ring_r5_t64"), ("linear", 128, 12304, 416, 8, "mx_wide_128x64"), ("swiglu", 65, 4112, 544, 4, "mx_wide_128x64"),
     ("linear", 200, 12304, 416, 4, "mx_wide_128x128"), ("swiglu", 65, 12304, 288, 8, "mx_wide_128x128"), ("add", 200, 12304, 1184, 8, "mx_wide_128x128"),
     ("add", 500, 12304, 288, 8, "mx_wide_256x128"), ("linear", 1000, 12304, 160, 4, "mx_wide_256x128"), ("swiglu", 257, 17424, 672, 4, "mx_wide_256x128"),
     ("add", 4100, 4112, 160, 4, "mx_wide_320x256"), ("swiglu", 1000, 8208, 416, 4, "mx_wide_320x256"), ("linear", 4100, 4112, 1184, 4, "mx_wide_320x256"),

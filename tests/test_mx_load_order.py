@@ -4,6 +4,7 @@ This test compiles the file to gfx950 assembly and counts them in every instance
 read of a slot has returned before the loads that refill it are issued."""
 from __future__ import annotations
 
+import concurrent.futures as cf
 import os
 import re
 import shutil
@@ -15,16 +16,22 @@ import pytest
 from w4_groupwise_gemm_amd import build as B
 
 
+def _asm(fmt, tmp):
+    out = os.path.join(tmp, f"mx_stream_{fmt}.s")
+    res = subprocess.run([B.HIPCC] + B.COMMON + B.DEVICE_FLAGS + [f"-DW4_MX_FMT={fmt}", "--cuda-device-only", "-S",
+                                                                  os.path.join(B.CSRC, "mx_stream.hip"), "-o", out],
+                         capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-2000:]
+    return open(out).read()
+
+
 @pytest.mark.skipif(not os.path.exists(B.HIPCC) and shutil.which(B.HIPCC) is None, reason="hipcc not available")
 def test_ring_loads_lie_between_their_waits():
     with tempfile.TemporaryDirectory() as tmp:
-        out = os.path.join(tmp, "mx_stream.s")
-        res = subprocess.run([B.HIPCC] + B.COMMON + B.DEVICE_FLAGS + ["--cuda-device-only", "-S", os.path.join(B.CSRC, "mx_stream.hip"),
-                                                                     "-o", out], capture_output=True, text=True)
-        assert res.returncode == 0, res.stderr[-2000:]
-        text = open(out).read()
+        with cf.ThreadPoolExecutor(2) as ex:
+            text = "".join(ex.map(lambda f: _asm(f, tmp), (4, 8)))
     seen = 0
-    for m in re.finditer(r"^_ZN2w412_GLOBAL__N_114mx_ring_kernelILi(\d)ELi(\d)ELi(\d)ELi(\d)ELi(\d)E\S*:", text, re.M):
+    for m in re.finditer(r"^_ZN2w412_GLOBAL__N_114mx_ring_kernelILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)E\S*:", text, re.M):
         fmt, rt, tt, nw, depth = map(int, m.groups())
         units = 8 // fmt
         loads = tt * 2 + rt * units
@@ -58,4 +65,4 @@ def test_ring_loads_lie_between_their_waits():
             elif l.startswith("buffer_load") and l.endswith("lds"):
                 assert not pending, (m.group(0)[:60], l)
         seen += 1
-    assert seen == 24, seen
+    assert seen == 48, seen

@@ -19,13 +19,14 @@ LIB = os.path.join(HERE, "libw4gemm.so")
 PROBE_LIB = os.path.join(HERE, "libw4probe.so")  # measurement support (read/copy/empty kernels)
 
 # (source, extra defines, object) -- stream.hip is compiled once per code width and epilogue,
-# narrow.hip once per code width
+# narrow.hip and regring.hip once per code width, mx_stream.hip once per activation format
 STREAM_PARTS = [("stream.hip", [f"-DW4_STREAM_BITS={b}", f"-DW4_STREAM_EPI={e}"], f"stream_b{b}_e{e}.o")
                 for b in (4, 5) for e in (0, 1, 2)]
 NARROW_PARTS = [("narrow.hip", [f"-DW4_NARROW_BITS={b}"], f"narrow_b{b}.o") for b in (4, 5)]
 REGRING_PARTS = [("regring.hip", [f"-DW4_REGRING_BITS={b}"], f"regring_b{b}.o") for b in (4, 5)]
-SOURCES = STREAM_PARTS + NARROW_PARTS + REGRING_PARTS + ["api.hip", "splitk.hip", "wide.hip", "bf16.hip", "a8.hip", "repack.cpp", "graphs.cpp",
-                                                           "mx_api.hip", "mx_quant.hip", "mx_stream.hip", "mx_wide.hip", "norm.hip", "mx_repack.cpp"]
+MX_STREAM_PARTS = [("mx_stream.hip", [f"-DW4_MX_FMT={f}"], f"mx_stream_f{f}.o") for f in (4, 8)]
+SOURCES = MX_STREAM_PARTS + STREAM_PARTS + NARROW_PARTS + REGRING_PARTS + ["api.hip", "splitk.hip", "wide.hip", "bf16.hip", "a8.hip", "repack.cpp", "graphs.cpp",
+                                                           "mx_api.hip", "mx_quant.hip", "mx_wide.hip", "norm.hip", "mx_repack.cpp"]
 PROBE_SOURCES = ["probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc" if os.path.exists("/opt/rocm/bin/hipcc") else "hipcc")

@@ -61,15 +61,24 @@ hipError_t launch_norm(int kind, bool bf16, const NormArgs& a, hipStream_t strea
 // token tiles of 16.  Wide (mx_wide.hip): one of kMxWide; the last (kMxWide320) for MXFP4 activations only.
 // A SwiGLU pair needs an even rt.  mx_*_lds: bytes of LDS a workgroup takes (at most kMxLds).
 constexpr size_t kMxLds = 160 * 1024;
+constexpr int kMxRows[] = {1, 2, 3, 4, 5, 6, 8, 10};
 size_t mx_stream_lds(int T, int K, int fmt, int rt);
-size_t mx_ring_lds(int K, int rt, int tt);
+size_t mx_ring_lds(int K, int fmt, int rt, int tt);
 struct MxTile {
   int rows, tokens;
 };
 constexpr MxTile kMxWide[] = {{64, 64}, {128, 64}, {128, 128}, {256, 128}, {320, 256}};
 constexpr int kMxWide320 = 4;
-hipError_t launch_mx_stream(int fmt, int rt, const MxArgs& a, hipStream_t stream);
-hipError_t launch_mx_ring(int fmt, int rt, int tt, const MxArgs& a, hipStream_t stream);
+hipError_t launch_mx_stream_4(int rt, const MxArgs& a, hipStream_t stream);  // MXFP4 activations
+hipError_t launch_mx_stream_8(int rt, const MxArgs& a, hipStream_t stream);  // MXFP8
+hipError_t launch_mx_ring_4(int rt, int tt, const MxArgs& a, hipStream_t stream);
+hipError_t launch_mx_ring_8(int rt, int tt, const MxArgs& a, hipStream_t stream);
+inline hipError_t launch_mx_stream(int fmt, int rt, const MxArgs& a, hipStream_t stream) {
+  return fmt == 4 ? launch_mx_stream_4(rt, a, stream) : launch_mx_stream_8(rt, a, stream);
+}
+inline hipError_t launch_mx_ring(int fmt, int rt, int tt, const MxArgs& a, hipStream_t stream) {
+  return fmt == 4 ? launch_mx_ring_4(rt, tt, a, stream) : launch_mx_ring_8(rt, tt, a, stream);
+}
 hipError_t launch_mx_wide(int fmt, int tile, const MxArgs& a, hipStream_t stream);
 
 // Status of the current device (W4_OK when it is a gfx950); defined in api.hip.

@@ -1,6 +1,7 @@
 // C ABI of the MX formats and the RMS norm: argument validation and launches.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 
@@ -68,18 +69,20 @@ const Cost kWideCost[2][5] = {
 
 // The cheapest kernel for the shape.  Few activations (up to 16 tokens): the streaming kernel, which
 // saves the launch for the quantisation (about 2.3 us) but quantises in every workgroup, m of them one
-// after another on a compute unit.  Measured at 12288 x 5120 (m = 1): 8 tokens 10.9 us against the ring's
-// 11.4, 16 tokens 13.7 against 11.9; at the 2 x 17408 x 5120 pair (m = 5): 4 tokens 23.0 against 24.6,
-// 8 tokens 27.8 against 25.0; at 5120 x 17408 (m = 1): 2 tokens 12.6 against 14.5, 4 tokens 15.7 against
-// 15.4.  Otherwise whichever of the ring (blocks of up to 64 tokens) and the wide tiles the fits above
-// name.
+// after another on a compute unit.  Measured at 12288 x 5120: 8 tokens 10.9 us against the ring's 11.4, 16
+// tokens 13.7 against 11.9; at the 2 x 17408 x 5120 pair: 8 tokens 22.1 against 22.6; at 5120 x 17408: 2
+// tokens 12.6 against 14.5, 4 tokens 15.7 against 15.4.  Otherwise whichever of the ring (blocks of up to
+// 64 tokens) and the wide tiles the fits above name.  Both take as many row tiles per workgroup as spare
+// the compute units a second round: the pair at 64 tokens 27.4 us with ten (one round), 38.4 with
+// four (three), 41.0 with two (five).
 constexpr double kStreamWork = 65536;  // T * K * (1 + m / 4)
 Route pick(int op, int T, int rows, int K, int fmt) {
   const int n = rows / 16, step = op == W4_OP_SWIGLU ? 2 : 1;
   Route best = {WIDE, 0, 0};
   double least = 1e30;
   if (T <= 16) {
-    for (int rt = step; rt <= 4; rt += step) {
+    for (int rt : w4::kMxRows) {
+      if (rt % step) continue;
       if (w4::mx_stream_lds(T, K, fmt, rt) > w4::kMxLds) continue;
       const double c = cost({0, 0.3 + rt}, (n + rt - 1) / rt);
       if (c < least) least = c, best = {STREAM, rt, 0};
@@ -89,8 +92,9 @@ Route pick(int op, int T, int rows, int K, int fmt) {
     least = 1e30;
   }
   const int tt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
-  for (int rt = step; rt <= 4; rt += step) {
-    if (w4::mx_ring_lds(K, rt, tt) > w4::kMxLds) continue;
+  for (int rt : w4::kMxRows) {
+    if (rt % step) continue;
+    if (w4::mx_ring_lds(K, fmt, rt, tt) > w4::kMxLds) continue;
     const Cost c = fmt == 4 ? Cost{0.12, 0.01 * tt + 0.047 * rt} : Cost{0.14, 0.0125 * tt + 0.056 * rt};
     const double v = cost(c, (int64_t)((n + rt - 1) / rt) * ((T + 16 * tt - 1) / (16 * tt)));
     if (v < least) least = v, best = {RING, rt, tt};
@@ -212,14 +216,18 @@ extern "C" size_t w4_linear_mx_workspace_bytes(int op, int T, int N, int K, int 
 
 extern "C" const char* w4_mx_route_name(int op, int T, int N, int K, int fmt) {
   if (!product_ok(op, T, N, K, fmt)) return nullptr;
-  static const char* const kStream[] = {"mx_stream_r1", "mx_stream_r2", "mx_stream_r3", "mx_stream_r4"};
-  static const char* const kRing[][4] = {{"mx_ring_r1_t16", "mx_ring_r2_t16", "mx_ring_r3_t16", "mx_ring_r4_t16"},
-                                         {"mx_ring_r1_t32", "mx_ring_r2_t32", "mx_ring_r3_t32", "mx_ring_r4_t32"},
-                                         {"mx_ring_r1_t64", "mx_ring_r2_t64", "mx_ring_r3_t64", "mx_ring_r4_t64"}};
+  static const char* const kStream[] = {"mx_stream_r1", "mx_stream_r2", "mx_stream_r3", "mx_stream_r4",
+                                        "mx_stream_r5", "mx_stream_r6", "mx_stream_r8", "mx_stream_r10"};
+#define RING_NAMES(t)                                                                                   \
+  {"mx_ring_r1_" t, "mx_ring_r2_" t, "mx_ring_r3_" t, "mx_ring_r4_" t, "mx_ring_r5_" t, "mx_ring_r6_" t, \
+   "mx_ring_r8_" t, "mx_ring_r10_" t}
+  static const char* const kRing[][8] = {RING_NAMES("t16"), RING_NAMES("t32"), RING_NAMES("t64")};
+#undef RING_NAMES
   static const char* const kWide[] = {"mx_wide_64x64", "mx_wide_128x64", "mx_wide_128x128", "mx_wide_256x128",
                                       "mx_wide_320x256"};
   const Route r = pick(op, T < 1 ? 1 : T, op == W4_OP_SWIGLU ? 2 * N : N, K, fmt);
-  return r.kind == STREAM ? kStream[r.rt - 1] : r.kind == RING ? kRing[r.tt == 4 ? 2 : r.tt - 1][r.rt - 1] : kWide[r.rt];
+  const int row = (int)(std::find(w4::kMxRows, w4::kMxRows + 8, r.rt) - w4::kMxRows);
+  return r.kind == STREAM ? kStream[row] : r.kind == RING ? kRing[r.tt == 4 ? 2 : r.tt - 1][row] : kWide[r.rt];
 }
 
 extern "C" int w4_quantize_mx(const uint16_t* x, int64_t ldx, int T, int K, int fmt, int dtype, void* workspace,

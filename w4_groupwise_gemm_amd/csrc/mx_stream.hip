@@ -3,6 +3,11 @@
 #include "mx.h"
 #include "tile32.h"
 
+// This file is compiled once per activation format (W4_MX_FMT = 4 or 8).
+#define W4_MX_CAT2(a, b) a##b
+#define W4_MX_CAT(a, b) W4_MX_CAT2(a, b)
+#define W4_MX_NAME(f) W4_MX_CAT(f##_, W4_MX_FMT)
+
 namespace w4 {
 namespace {
 
@@ -288,9 +293,10 @@ __global__ __launch_bounds__(64 * NW) void mx_ring_kernel(MxArgs a, int groups) 
 }
 
 constexpr int kStreamWaves = 8, kStreamDepth = 2;
-// Waves of the ring kernel by token tiles: eight while two slots each leave room for the scale bytes of
-// long rows, four at 64 tokens.
-constexpr int ring_waves(int tt) { return tt == 4 ? 4 : 8; }
+// Waves of the ring kernel: eight while two slots each leave room for the scale bytes of long rows, four
+// at 64 tokens; and four where a unit's weights (two k-blocks with MXFP4) take more registers than two
+// waves a SIMD have.
+constexpr int ring_waves(int fmt, int rt, int tt) { return tt == 4 || (fmt == 4 && rt >= 6) ? 4 : 8; }
 constexpr int kRingDepth = 2;
 
 template <int FMT, int RT>
@@ -307,9 +313,9 @@ hipError_t run_stream(const MxArgs& a, hipStream_t stream) {
 template <int FMT, int RT, int TT>
 hipError_t run_ring(const MxArgs& a, hipStream_t stream) {
   const int groups = (a.rows / 16 + RT - 1) / RT, blocks = (a.T + 16 * TT - 1) / (16 * TT);
-  constexpr int NW = ring_waves(TT);
+  constexpr int NW = ring_waves(FMT, RT, TT);
   return launch_kernel(&mx_ring_kernel<FMT, RT, TT, NW, kRingDepth>, dim3(groups * blocks), dim3(64 * NW),
-                       mx_ring_lds(a.K, RT, TT), stream, a, groups);
+                       mx_ring_lds(a.K, FMT, RT, TT), stream, a, groups);
 }
 
 template <int FMT, int RT>
@@ -322,30 +328,39 @@ hipError_t ring_rt(int tt, const MxArgs& a, hipStream_t stream) {
   }
 }
 
-template <int FMT>
-hipError_t stream_fmt(int rt, const MxArgs& a, hipStream_t stream) {
+}  // namespace
+
+hipError_t W4_MX_NAME(launch_mx_stream)(int rt, const MxArgs& a, hipStream_t stream) {
+  constexpr int FMT = W4_MX_FMT;
   switch (rt) {
     case 1: return run_stream<FMT, 1>(a, stream);
     case 2: return run_stream<FMT, 2>(a, stream);
     case 3: return run_stream<FMT, 3>(a, stream);
     case 4: return run_stream<FMT, 4>(a, stream);
+    case 5: return run_stream<FMT, 5>(a, stream);
+    case 6: return run_stream<FMT, 6>(a, stream);
+    case 8: return run_stream<FMT, 8>(a, stream);
+    case 10: return run_stream<FMT, 10>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }
 
-template <int FMT>
-hipError_t ring_fmt(int rt, int tt, const MxArgs& a, hipStream_t stream) {
+hipError_t W4_MX_NAME(launch_mx_ring)(int rt, int tt, const MxArgs& a, hipStream_t stream) {
+  constexpr int FMT = W4_MX_FMT;
   switch (rt) {
     case 1: return ring_rt<FMT, 1>(tt, a, stream);
     case 2: return ring_rt<FMT, 2>(tt, a, stream);
     case 3: return ring_rt<FMT, 3>(tt, a, stream);
     case 4: return ring_rt<FMT, 4>(tt, a, stream);
+    case 5: return ring_rt<FMT, 5>(tt, a, stream);
+    case 6: return ring_rt<FMT, 6>(tt, a, stream);
+    case 8: return ring_rt<FMT, 8>(tt, a, stream);
+    case 10: return ring_rt<FMT, 10>(tt, a, stream);
     default: return hipErrorInvalidValue;
   }
 }
 
-}  // namespace
-
+#if W4_MX_FMT == 4
 size_t mx_stream_lds(int T, int K, int fmt, int rt) {
   size_t tp = 1;
   while (tp < (size_t)T) tp *= 2;
@@ -354,18 +369,12 @@ size_t mx_stream_lds(int T, int K, int fmt, int rt) {
   return need > red ? need : red;
 }
 
-size_t mx_ring_lds(int K, int rt, int tt) {
-  const size_t ring = (size_t)ring_waves(tt) * kRingDepth * tt * 2048, red = (size_t)ring_waves(tt) * rt * tt * 1024;
+size_t mx_ring_lds(int K, int fmt, int rt, int tt) {
+  const size_t ring = (size_t)ring_waves(fmt, rt, tt) * kRingDepth * tt * 2048, red = (size_t)ring_waves(fmt, rt, tt) * rt * tt * 1024;
   const size_t b = ring + lds_copy(tt * 16 * mx_scale_stride(K)) + lds_copy((size_t)rt * w4layout::num_kblocks(K) * 64);
   return b > red ? b : red;
 }
 
-hipError_t launch_mx_stream(int fmt, int rt, const MxArgs& a, hipStream_t stream) {
-  return fmt == 4 ? stream_fmt<4>(rt, a, stream) : stream_fmt<8>(rt, a, stream);
-}
-
-hipError_t launch_mx_ring(int fmt, int rt, int tt, const MxArgs& a, hipStream_t stream) {
-  return fmt == 4 ? ring_fmt<4>(rt, tt, a, stream) : ring_fmt<8>(rt, tt, a, stream);
-}
+#endif
 
 }  // namespace w4
