@@ -165,12 +165,13 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4 * WG_PER_CU) void mx_wide_k
     for (int i = 0; i < S::kCL; ++i)
       to_lds16(cr[i], st + min(wave + kWaves * i, S::kCN - 1) * 1024, last ? vlast[i] : voff[i], kb * step[i]);
   };
-  // (past the last columns the last ones again, which nothing reads)
+  // (past the last columns the last ones again, which nothing reads; the last four k-blocks may end inside
+  // the 256 bytes, so the whole offset is the lane's, which the resource's bounds check covers)
   auto load_scales = [&](int q, int last) {
 #pragma unroll
     for (int i = 0; i < S::kSL; ++i)
-      to_lds16(sr[i], scales + (q & 1) * S::kScales + min(wave + kWaves * i, S::kSN - 1) * 1024, soff[i],
-               min(q, last) * sstep[i]);
+      to_lds16(sr[i], scales + (q & 1) * S::kScales + min(wave + kWaves * i, S::kSN - 1) * 1024,
+               soff[i] + min(q, last) * sstep[i], 0);
   };
 
   f32x16 acc[MT][NT] = {};
