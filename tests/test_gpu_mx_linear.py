@@ -301,3 +301,30 @@ def test_norm_feeds_the_a8_route():
         ref = oracle.linear(a, *canon(wset), 4)
         # a is rounded to bf16 (2^-9 relative each): rel L2 below 2^-8
         assert oracle.rel_l2(exact64(y), ref) <= 2.0 ** -8
+
+
+def test_weights_that_shrank_after_a_call_are_refused():
+    c = Case("linear", 4, 64, 128, "fp16", 8)
+    c.check(c.run())
+    c.pw.w.resize_(c.pw.w.numel() // 2)
+    with pytest.raises(ValueError):
+        c.run()
+    c = Case("add", 4, 64, 128, "fp16", 8)
+    c.check(c.run())
+    c.pw.N = 128
+    with pytest.raises(ValueError):
+        w4.linear_mx(c.x, c.pw)
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+
+    c = Case("linear", 4, 64, 128, "fp16", 8)
+    weight = torch.ones(128, dtype=torch.float16, device=DEV)
+    q = w4.quantize_mx(c.x)
+    for call in (lambda s: c.run(stream=s), lambda s: c.run(q, stream=s), lambda s: w4.quantize_mx(c.x, stream=s),
+                 lambda s: w4.dequantize_mx(q, stream=s), lambda s: w4.rmsnorm(c.x, weight, stream=s),
+                 lambda s: w4.rmsnorm_a8(c.x, weight, stream=s), lambda s: w4.rmsnorm_mx(c.x, weight, stream=s)):
+        with pytest.raises(ValueError):
+            call(Elsewhere())

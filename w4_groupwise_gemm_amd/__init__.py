@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -606,9 +607,6 @@ class PackedMX:
     N: int             # output width (of each of gate/up for a pair)
     K: int
     pair: bool = False
-    # what the calls have worked out: the tensors found to fit, and workspace sizes by (T, fmt)
-    _fits: tuple = dataclasses.field(default=(), init=False, repr=False, compare=False)
-    _need: dict = dataclasses.field(default_factory=dict, init=False, repr=False, compare=False)
 
     @property
     def nbytes_stream(self) -> int:
@@ -713,6 +711,8 @@ def _there(device, stream, call, *args, **kwargs):
     stream, so that what the call allocates belongs to the stream that uses it."""
     if not isinstance(device, _torch.device) or device.type != "cuda":
         raise ValueError("the tensors must be on a GPU")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     with _torch.cuda.device(device), _torch.cuda.stream(stream):
         return call(*args, **kwargs)
 
@@ -879,13 +879,9 @@ def _linear_mx(op: int, x, pw: PackedMX, residual, fmt, out, workspace, dtype, s
         _check_fmt(fmt)
         dtype, xp = x.dtype, x.data_ptr()
     code = _dtype16(dtype)
-    fits = pw._fits
-    if not (fits and fits[0] is w and fits[1] is scales and fits[2:] == (N, K, pair, device)):
-        blocks = (2 * N if pair else N) // 16 * ((K + 127) // 128)
-        _is(w, "packed codes", (blocks * 1024,), torch.uint8, device)
-        _is(scales, "packed scales", (blocks * 64,), torch.uint8, device)
-        pw._fits = (w, scales, N, K, pair, device)
-        pw._need = {}
+    blocks = (2 * N if pair else N) // 16 * ((K + 127) // 128)
+    _is(w, "packed codes", (blocks * 1024,), torch.uint8, device)
+    _is(scales, "packed scales", (blocks * 64,), torch.uint8, device)
     if out is None:
         out = w.new_empty((T, N), dtype=dtype) if quantised else x.new_empty((T, N))
     else:
@@ -895,11 +891,7 @@ def _linear_mx(op: int, x, pw: PackedMX, residual, fmt, out, workspace, dtype, s
     if quantised:
         wp, wn = ws.data_ptr(), ws.numel()
     else:
-        need = pw._need.get((T, fmt))
-        if need is None:
-            need = L.w4_linear_mx_workspace_bytes(op, T, N, K, fmt)
-            if len(pw._need) < 4096:
-                pw._need[T, fmt] = need
+        need = _linear_mx_need(op, T, N, K, fmt)
         if workspace is None and need == 0:
             wp, wn = None, 0
         else:
@@ -933,6 +925,11 @@ def linear_swiglu_mx(x, pw: PackedMX, fmt=None, out=None, workspace=None, dtype=
 def linear_add_mx(x, pw: PackedMX, residual, fmt=None, out=None, workspace=None, dtype=None, stream=None):
     """out[T, N] = x . W^T + residual (out may be residual); otherwise as linear_mx."""
     return _linear_mx(OP_ADD, x, pw, residual, fmt, out, workspace, dtype, stream)
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_mx_need(op: int, T: int, N: int, K: int, fmt: int) -> int:
+    return int(lib().w4_linear_mx_workspace_bytes(op, T, N, K, fmt))
 
 
 def linear_mx_workspace_bytes(op: int, T: int, N: int, K: int, fmt: int) -> int:
