@@ -190,7 +190,7 @@ constexpr int min_waves(int vpt) { return vpt == 1 ? 7 : vpt == 2 ? 6 : vpt == 4
 
 // VPT vectors of 8 columns per lane in registers.  A workgroup takes rows blockIdx.x, + gridDim.x, ..: the
 // next row's loads are issued before this row's sum.  Long rows (VPT >= 4) keep the weight in registers
-// (4096 x 17408: 114 us, read again for each row 134); for short ones the waves that those registers
+// (4096 x 17408 with the residual: 108 us, read again for each row 113); for short ones the waves that those registers
 // cost are worth more (4096 x 5120 without residual: 21.1 us read again, 23.3 kept).
 template <int KIND, bool BF, int VPT>
 __global__ __launch_bounds__(max_threads(VPT), min_waves(VPT)) void norm_kernel(NormArgs a) {
@@ -249,15 +249,19 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
 
 constexpr int kCUs = 256;
 
-// Threads and vectors per lane.  Few rows: as many lanes as the row has vectors, for latency.  Many rows:
-// at most 320 lanes (4096 x 5120 with the residual, 16-bit output: 35.8 us; 640 lanes of one vector
-// 38.0, 192 lanes of four 39.8), so that a compute unit has more rows on their way, and two rows or
-// more per workgroup (one where a lane holds four vectors or more: 4096 x 17408 114 us against 122).
+// Threads and vectors per lane.  As many lanes as a row has vectors, for latency.  With many rows (T > 512)
+// and more than 320 vectors two to a lane, so that a compute unit has more rows on their way (4096 x 5120 with
+// the residual, 16-bit output: 34.9 us; one to a lane 37.7; the other way round at 512 rows, 6.8 against
+// 6.2).  More vectors to a lane only where the lanes run out: at most 320 lanes with four or eight took
+// 17408 columns 113 us against 108 at 4096 rows (to int8 163 against 108) and 42 against 34 at 1024, 12288
+// columns to MXFP8 84 against 72; 6144 columns gained up to 10 % from it at 1024 rows.  Two rows or more per
+// workgroup (one where a lane holds four vectors or more: 1024 x 17408 34.0 us against 37.5, 4096 x
+// 17408 without residual 56.2 against 59.3).
 template <int KIND, bool BF>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   const int64_t nvec = ((int64_t)a.K + 7) / 8;
   int vpt = 1;
-  while (vpt < 8 && nvec > (int64_t)vpt * (a.T <= 2 * kCUs ? max_threads(vpt) : 320)) vpt *= 2;
+  while (vpt < 8 && nvec > (int64_t)vpt * (vpt == 1 && a.T > 2 * kCUs ? 320 : max_threads(vpt))) vpt *= 2;
   const int64_t threads = ((nvec + vpt - 1) / vpt + 63) / 64 * 64;
   const int resident = kCUs * (threads >= 1024 ? 2 : (int)(2048 / threads));
   const int most = resident * (vpt >= 4 ? 1 : 2);
